@@ -8,6 +8,15 @@ not on a CUDA device, the call raises.
     qw = quantize_nf4(w)                     # w: [N, K] bf16 on cuda
     y = linear_fwd(x, qw, A, B, s)           # x: [T, K], A: [r, K], B: [N, r]
     dx, dA, dB = linear_bwd(dy, x, qw, A, B, s)
+
+The same backward from an activation kept in 8 bits, and the int8 product that
+serves a merged weight:
+
+    y, u = linear_fwd_save(x, qw, A, B, s)
+    x8 = quantize_int8(x, group=128)         # instead of keeping x
+    dx, dA, dB = linear_bwd_saved_int8(dy, x8, qw, A, B, s, u)
+    w8 = quantize_int8(merge_adapter(qw, A, B, s))
+    y = linear_int8(x, w8)                   # x quantized per token in the call
 """
 from __future__ import annotations
 
@@ -23,7 +32,8 @@ __all__ = ["QuantizedNF4", "nf4_codebook", "storage_bytes", "quantize_nf4", "deq
            "linear_fwd", "linear_bwd", "linear_fwd_save", "linear_bwd_saved", "saved_u_bytes",
            "linear_fwd_noalloc", "noalloc_get_error", "wait_selftest", "workspace", "workspace_bytes",
            "get_error", "adam_step", "PagedBuffer", "quantize_nf4_into", "linear_fwd_decode_batch",
-           "QLoraError", "lib"]
+           "QuantizedInt8", "quantize_int8", "quantize_int8_into", "dequantize_int8", "linear_int8",
+           "linear_bwd_saved_int8", "QLoraError", "lib"]
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -102,13 +112,27 @@ def workspace(device: torch.device, nbytes: int) -> torch.Tensor:
     return ws
 
 
+_STATUS: dict = {}
+
+
+def _status(device: torch.device) -> int | None:
+    """Address of `device`'s status word for the calls that take it apart from
+    their scratch: made once (not while a graph is being captured) and kept."""
+    st = _STATUS.get(device)
+    if st is None:
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        st = _STATUS[device] = torch.zeros(256, dtype=torch.uint8, device=device)
+        torch.cuda.current_stream(device).synchronize()   # other streams may be the first to use it
+    return st.data_ptr()
+
+
 def get_error(device=None) -> None:
     """Synchronize and raise if a kernel recorded a device-side failure."""
     dev = torch.device(device if device is not None else torch.cuda.current_device())
-    ws = _WS.get(dev)
-    if ws is None:
-        return
-    check("qlora_get_error", lib().qlora_get_error(C.c_void_p(ws.data_ptr()), _stream(dev)))
+    for ws in (_WS.get(dev), _STATUS.get(dev)):
+        if ws is not None:
+            check("qlora_get_error", lib().qlora_get_error(C.c_void_p(ws.data_ptr()), _stream(dev)))
 
 
 def quantize_nf4(w: torch.Tensor, codebook=None, blocksize: int = 64, dq_block: int = 256,
@@ -376,6 +400,164 @@ def linear_bwd_saved(dy: torch.Tensor, x: torch.Tensor, qw: QuantizedNF4, A: tor
         C.c_void_p(B.data_ptr()), r, float(s), C.c_void_p(u_saved.data_ptr()), C.c_void_p(dx.data_ptr()),
         C.c_void_p(dA.data_ptr()), C.c_void_p(dB.data_ptr()), C.c_void_p(ws.data_ptr()), ws.numel(),
         _stream(dev)))
+    return dx, dA, dB
+
+
+# --------------------------------------------------------------------------
+# 8 bits: checkpoints of activations, and the int8 product of a merged weight
+# --------------------------------------------------------------------------
+_INT8_GROUP = 128
+
+
+class QuantizedInt8:
+    """A matrix in signed 8-bit codes (qlora_int8_matrix): value = code * scale,
+    one FP32 scale per row (group 0) or per 128 consecutive columns of a row
+    (group 128).  codes: int8 [rows, cols]; scales: float32 [groups, rows]."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "group", "device", "_struct", "_ref")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, group: int = 0):
+        _need_cuda("codes", codes, dtype=torch.int8)
+        _need_cuda("scales", scales, dtype=torch.float32)
+        if codes.dim() != 2:
+            raise ValueError("codes must be 2-D [rows, cols]")
+        if group not in (0, _INT8_GROUP):
+            raise ValueError(f"group must be 0 (one scale a row) or {_INT8_GROUP}")
+        rows, cols = codes.shape
+        groups = -(-cols // group) if group else 1
+        if tuple(scales.shape) != (groups, rows):
+            raise ValueError(f"scales must be [{groups}, {rows}], got {list(scales.shape)}")
+        if scales.device != codes.device:
+            raise ValueError(f"scales is on {scales.device}, codes on {codes.device}")
+        self.codes, self.scales, self.rows, self.cols, self.group = codes, scales, rows, cols, group
+        self.device = codes.device
+        self._struct = _lib.Int8Matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, group)
+        self._ref = C.byref(self._struct)
+        _status(self.device)   # before any capture
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+def _int8_call(device: torch.device, fn: str, *args) -> None:
+    """Call an entry point with `device` current (its launches go there)."""
+    if device.index == torch.cuda.current_device():
+        st = getattr(lib(), fn)(*args)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(lib(), fn)(*args)
+    if st:
+        check(fn, st)
+
+
+def quantize_int8(x: torch.Tensor, group: int = 0) -> QuantizedInt8:
+    """x[rows, cols] (BF16, cols % 16 == 0) in 8 bits: code = round(x / scale)
+    to nearest even, scale = max |x| / 127 over each row (group 0: what
+    linear_int8 takes, per token or per output channel) or over each 128
+    columns of a row (group 128: closer to x where a row has outlier channels).
+    A group with an infinity or a NaN has scale NaN."""
+    _need_cuda("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [rows, cols]")
+    if group not in (0, _INT8_GROUP):
+        raise ValueError(f"group must be 0 (one scale a row) or {_INT8_GROUP}")
+    rows, cols = x.shape
+    dev = x.device
+    out = QuantizedInt8(torch.empty(rows, cols, dtype=torch.int8, device=dev),
+                        torch.empty(-(-cols // group) if group else 1, rows, dtype=torch.float32, device=dev), group)
+    _int8_call(dev, "qlora_quantize_int8", x.data_ptr(), rows, cols, group, out._ref, _stream(dev))
+    return out
+
+
+def quantize_int8_into(x: torch.Tensor, out: QuantizedInt8) -> QuantizedInt8:
+    """Quantize x again into the buffers of an existing QuantizedInt8 of the
+    same shape (no allocation)."""
+    _need_cuda("x", x)
+    if tuple(x.shape) != (out.rows, out.cols) or x.device != out.device:
+        raise ValueError(f"x must be [{out.rows}, {out.cols}] on {out.device}")
+    _int8_call(out.device, "qlora_quantize_int8", x.data_ptr(), out.rows, out.cols, out.group, out._ref,
+               _stream(out.device))
+    return out
+
+
+def dequantize_int8(q8: QuantizedInt8, out: torch.Tensor | None = None) -> torch.Tensor:
+    """BF16(code * scale) as a [rows, cols] tensor."""
+    dev = q8.device
+    if out is None:
+        out = torch.empty(q8.rows, q8.cols, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out("out", out, (q8.rows, q8.cols), dev)
+    _int8_call(dev, "qlora_dequantize_int8", q8._ref, out.data_ptr(), _stream(dev))
+    return out
+
+
+def linear_int8(x, w8: QuantizedInt8, out: torch.Tensor | None = None) -> torch.Tensor:
+    """y = xq wq^T (BF16): the INT32 product of 8-bit codes, scaled per token
+    and per output channel.  x: BF16 [T, K], quantized per token in the call,
+    or a QuantizedInt8 (group 0) that several products share."""
+    if not isinstance(w8, QuantizedInt8) or w8.group != 0:
+        raise ValueError("w8 must be a QuantizedInt8 with one scale a row (group 0)")
+    dev, K = w8.device, w8.cols
+    given = isinstance(x, QuantizedInt8)
+    if given:
+        if x.group != 0:
+            raise ValueError("x must have one scale a token (group 0)")
+        T, xk = x.rows, x.cols
+    else:
+        _need_cuda("x", x)
+        if x.dim() != 2:
+            raise ValueError(f"x must be [T, {K}]")
+        T, xk = x.shape
+    if xk != K:
+        raise ValueError(f"x must be [T, {K}]")
+    if x.device != dev:
+        raise ValueError(f"x is on {x.device}, w8 on {dev}")
+    if out is None:
+        out = torch.empty(T, w8.rows, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out("out", out, (T, w8.rows), dev)
+    if given:
+        _int8_call(dev, "qlora_linear_int8_q", x._ref, w8._ref, out.data_ptr(), _status(dev), _stream(dev))
+    else:
+        # the quantized tokens live for this call only (the allocator hands the
+        # block to work that follows on this stream, or keeps it in the pool of
+        # the graph being captured)
+        n = lib().qlora_linear_int8_scratch_bytes(T, K)
+        scratch = torch.empty(n, dtype=torch.uint8, device=dev)
+        _int8_call(dev, "qlora_linear_int8", x.data_ptr(), T, w8._ref, out.data_ptr(), scratch.data_ptr(), n,
+                   _status(dev), _stream(dev))
+    return out
+
+
+def linear_bwd_saved_int8(dy: torch.Tensor, x8: QuantizedInt8, qw: QuantizedNF4, A: torch.Tensor, B: torch.Tensor,
+                          s: float, u_saved: torch.Tensor, outs=None):
+    """linear_bwd_saved with the activation kept in 8 bits (quantize_int8 of
+    the forward's x, either group): dA is formed from the codes and scales as
+    they are, dX and dB do not depend on x."""
+    if not isinstance(x8, QuantizedInt8):
+        raise ValueError("x8 must be a QuantizedInt8")
+    for n, t in (("A", A), ("B", B)):
+        _need_cuda(n, t)
+    dev, T = x8.device, x8.rows
+    if x8.cols != qw.cols:
+        raise ValueError(f"x8 must be [T, {qw.cols}]")
+    r = A.shape[0]
+    if tuple(A.shape) != (r, qw.cols) or tuple(B.shape) != (qw.rows, r):
+        raise ValueError(f"A must be [r, {qw.cols}] and B [{qw.rows}, r]")
+    for n, t in (("A", A), ("B", B), ("qw", qw.codes)):
+        if t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, x8 on {dev}")
+    _check_out("dy", dy, (T, qw.rows), dev)
+    _need_cuda("u_saved", u_saved, dtype=torch.uint8)
+    if u_saved.numel() < saved_u_bytes(T, r) or u_saved.device != dev:
+        raise ValueError(f"u_saved must hold {saved_u_bytes(T, r)} bytes on {dev}")
+    dx, dA, dB = _bwd_outs(outs, T, qw, r, dev)
+    n = workspace_bytes(OP_BWD, T, qw.rows, qw.cols, r)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)   # for this call only, as linear_int8's scratch
+    st = qw.struct()
+    _int8_call(dev, "qlora_linear_bwd_saved_int8", dy.data_ptr(), x8._ref, C.byref(st), A.data_ptr(), B.data_ptr(), r,
+               float(s), u_saved.data_ptr(), dx.data_ptr(), dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), n,
+               _status(dev), _stream(dev))
     return dx, dA, dB
 
 

@@ -35,6 +35,12 @@ class AdamHParams(C.Structure):
                 ("weight_decay", C.c_float), ("step", C.c_int32)]
 
 
+class Int8Matrix(C.Structure):
+    """Mirror of qlora_int8_matrix."""
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("group", C.c_int32)]
+
+
 class FwdProblem(C.Structure):
     """Mirror of qlora_fwd_problem."""
     _fields_ = [("x", C.c_void_p), ("qw", C.POINTER(NF4Weight)), ("A", C.c_void_p), ("B", C.c_void_p),
@@ -84,6 +90,18 @@ SIGNATURES = {
     "qlora_linear_bwd_saved": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.POINTER(NF4Weight), C.c_void_p,
                                          C.c_void_p, C.c_int32, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p,
                                          C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "qlora_int8_storage_bytes": (C.c_int, [C.c_int64, C.c_int64, C.c_int32, C.POINTER(C.c_size_t),
+                                           C.POINTER(C.c_size_t)]),
+    "qlora_quantize_int8": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int32, C.POINTER(Int8Matrix), C.c_void_p]),
+    "qlora_dequantize_int8": (C.c_int, [C.POINTER(Int8Matrix), C.c_void_p, C.c_void_p]),
+    "qlora_linear_int8_scratch_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
+    "qlora_linear_int8": (C.c_int, [C.c_void_p, C.c_int64, C.POINTER(Int8Matrix), C.c_void_p, C.c_void_p, C.c_size_t,
+                                    C.c_void_p, C.c_void_p]),
+    "qlora_linear_int8_q": (C.c_int, [C.POINTER(Int8Matrix), C.POINTER(Int8Matrix), C.c_void_p, C.c_void_p,
+                                      C.c_void_p]),
+    "qlora_linear_bwd_saved_int8": (C.c_int, [C.c_void_p, C.POINTER(Int8Matrix), C.POINTER(NF4Weight), C.c_void_p,
+                                              C.c_void_p, C.c_int32, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p,
+                                              C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
     "qlora_wait_selftest": (C.c_int, [C.c_void_p, C.c_size_t, C.c_uint32, C.c_void_p]),
     "qlora_adam_step": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
                                   C.POINTER(AdamHParams), C.c_void_p]),

@@ -69,13 +69,19 @@ enum KernelId : int32_t {
   K_LORA_DU_DB = 12,    // dU and dB from one read of dY (block partial sums)
   K_ADAM = 13,          // the adapters' optimizer step
   K_LORA_DU_DB_SUM = 14,  // the sums of those partials: dU planes and dB
-  K_COUNT = 15,
+  K_UNUSED = 15,        // callers tell an id past the NF4 layer's kernels by this number
+  K_QUANTIZE_INT8 = 16,
+  K_DEQUANTIZE_INT8 = 17,
+  K_INT8_GEMM = 18,
+  K_DA_INT8 = 19,       // dA from an 8-bit activation
+  K_COUNT = 20,
 };
 
 const char *kKernelNames[K_COUNT] = {"quantize_nf4_dq", "dequantize_nf4", "lora_u",       "lora_du",
                                      "lora_dB",         "lora_dA",        "nf4_gemm_fwd", "nf4_gemm_bwd_dx",
                                      "nf4_gemv_fwd",    "lora_u+du",      "lora_dB+dA",   "merge_adapter",
-                                     "lora_du+dB",      "adam_step",      "lora_du+dB_sum"};
+                                     "lora_du+dB",      "adam_step",      "lora_du+dB_sum", "unknown",      "quantize_int8",
+                                     "dequantize_int8", "int8_gemm",      "lora_dA_int8"};
 
 struct TraceScope {
   cudaStream_t st;
@@ -816,9 +822,11 @@ static qlora_status linear_fwd_impl(const void *x, int64_t T, const qlora_nf4_we
 
 // The backward after validation (T > 0).  u_saved (optional): the planes the
 // forward saved; without them sU is recomputed from X.
-static qlora_status linear_bwd_impl(const void *dy, const void *x, int64_t T, const qlora_nf4_weight *qw,
-                                    const void *A, const void *B, int32_t r, float s, const void *u_saved, void *dx,
-                                    void *dA, void *dB, void *ws, cudaStream_t st) {
+// x8 (optional, with u_saved): the activation in 8 bits in the place of x.
+static qlora_status linear_bwd_impl(const void *dy, const void *x, const qlora_int8_matrix *x8, int64_t T,
+                                    const qlora_nf4_weight *qw, const void *A, const void *B, int32_t r, float s,
+                                    const void *u_saved, void *dx, void *dA, void *dB, void *ws, uint32_t *status,
+                                    cudaStream_t st) {
   const int64_t N = qw->rows, K = qw->cols;
   uint8_t *w8 = static_cast<uint8_t *>(ws);
   const WsLayout L = ws_layout(QLORA_OP_BWD, T, N, K, r);
@@ -862,6 +870,9 @@ static qlora_status linear_bwd_impl(const void *dy, const void *x, int64_t T, co
   const bool fused = dudb_geom(T, N, r, kSplitSms, gdd);
   DuDbArgs fa;
   CUtensorMap fm_dy, fm_b, fm_su_hi, fm_su_lo;
+  DaInt8Geom gx8;
+  DaInt8Args ax8;
+  CUtensorMap xm_x, xm_hi, xm_lo;
   qlora_status rs;
   if (!u_saved && !fused) {
     // one grid: sU = s X A^T, transposed, as hi + lo planes, with dU; then
@@ -916,7 +927,7 @@ static qlora_status linear_bwd_impl(const void *dy, const void *x, int64_t T, co
       fa.duT_lo = ad.t_lo;
       fa.ldt = ad.ldt;
       fa.dB = static_cast<uint16_t *>(dB);
-      fa.status = reinterpret_cast<uint32_t *>(ws);
+      fa.status = status;
       if (!make_map_bf16(&fm_dy, dy, T, N, N, 128, 64, true) || !make_map_bf16(&fm_b, bq, N, r, ldb, 64, 64, true) ||
           !make_map_bf16(&fm_su_hi, su_hi, r, T, Tp, gdd.rb, 64, true) ||
           !make_map_bf16(&fm_su_lo, su_lo, r, T, Tp, gdd.rb, 64, true))
@@ -938,13 +949,32 @@ static qlora_status linear_bwd_impl(const void *dy, const void *x, int64_t T, co
       have_mid = true;
     }
     // then dA
-    const TcProduct ta = {K_LORA_DA, x, K, true, plane(L.duT_hi), plane(L.duT_lo), Tp, false, geom_da(T, K, r)};
-    rs = prepare_single_tc(ta, aa, w8, L, second);
+    if (x8) {
+      gx8 = da_int8_geom(T, K, r, kSplitSms);
+      memset(&ax8, 0, sizeof(ax8));
+      ax8.T = T;
+      ax8.K = K;
+      ax8.R = r;
+      ax8.raw_stages = gx8.raw_stages;
+      ax8.t_per_split = gx8.t_per_split;
+      ax8.scales = x8->scales;
+      ax8.grouped = x8->group != 0 ? 1 : 0;
+      ax8.dA = static_cast<uint16_t *>(dA);
+      ax8.status = status;
+      if (!make_map_u8(&xm_x, x8->codes, T, K, K, 64, 128) ||
+          !make_map_bf16(&xm_hi, plane(L.duT_hi), r, T, Tp, gx8.nb, 64, true) ||
+          !make_map_bf16(&xm_lo, plane(L.duT_lo), r, T, Tp, gx8.nb, 64, true))
+        return QLORA_ERR_CUDA;
+      rs = QLORA_OK;
+    } else {
+      const TcProduct ta = {K_LORA_DA, x, K, true, plane(L.duT_hi), plane(L.duT_lo), Tp, false, geom_da(T, K, r)};
+      rs = prepare_single_tc(ta, aa, w8, L, second);
+    }
   }
   if (rs != QLORA_OK) return rs;
   // dX = dY W' + dU A
   GemmLaunch gl;
-  rs = prepare_gemm(1, qw, dy, plane(L.du_row), r64, A, r, dx, T, reinterpret_cast<uint32_t *>(ws), gl);
+  rs = prepare_gemm(1, qw, dy, plane(L.du_row), r64, A, r, dx, T, status, gl);
   if (rs != QLORA_OK) return rs;
   // The last launch (dA, or dB with dA) needs only dU's planes and the
   // inputs, not dX: it follows the dX GEMM as a programmatic dependent that
@@ -953,6 +983,7 @@ static qlora_status linear_bwd_impl(const void *dy, const void *x, int64_t T, co
   // the launch before the GEMM, which wrote those planes, has completed.)
   second.a0.dep_late = 1;
   second.a1.dep_late = 1;
+  for (TcLaunch *l : {&first, &mid, &second, &ul}) l->a0.status = l->a1.status = status;
 
   if (pad_b && launch_pad_cols(static_cast<const uint16_t *>(B), N, r, plane(L.bpad), static_cast<int>(r64), st,
                                num_sms_current()) != cudaSuccess)
@@ -982,6 +1013,12 @@ static qlora_status linear_bwd_impl(const void *dy, const void *x, int64_t T, co
   }
   rs = launch_gemm(gl, st);
   if (rs != QLORA_OK) return rs;
+  if (x8) {
+    const double tk = static_cast<double>(T) * K;
+    TraceScope ts(K_DA_INT8, 4.0 * tk * r, tk + 4.0 * T * (x8->group != 0 ? (K + kInt8Group - 1) / kInt8Group : 1), st);
+    return launch_da_int8(ax8, gx8, xm_x, xm_hi, xm_lo, st, g_trace.recs == nullptr) == cudaSuccess ? QLORA_OK
+                                                                                                    : QLORA_ERR_CUDA;
+  }
   return launch_tc(second, st);
 }
 
@@ -1003,7 +1040,8 @@ static qlora_status linear_bwd_entry(const void *dy, const void *x, int64_t T, c
     if (cudaMemsetAsync(dB, 0, static_cast<size_t>(N) * r * 2, st) != cudaSuccess) return QLORA_ERR_CUDA;
     return QLORA_OK;
   }
-  return linear_bwd_impl(dy, x, T, qw, A, B, r, s, want_saved ? u_saved : nullptr, dx, dA, dB, ws, st);
+  return linear_bwd_impl(dy, x, nullptr, T, qw, A, B, r, s, want_saved ? u_saved : nullptr, dx, dA, dB, ws,
+                         static_cast<uint32_t *>(ws), st);
 }
 
 qlora_status qlora_linear_fwd(const void *x, int64_t T, const qlora_nf4_weight *qw, const void *A, const void *B,
@@ -1242,6 +1280,182 @@ qlora_status qlora_wait_selftest(void *ws, size_t ws_bytes, uint32_t limit_us, v
   wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint32_t *>(ws),
                                                                         1000ull * limit_us);
   return cudaGetLastError() == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit row format: checkpoints of activations, and the int8 product
+// ---------------------------------------------------------------------------
+qlora_status qlora_int8_storage_bytes(int64_t rows, int64_t cols, int32_t group, size_t *codes_bytes,
+                                      size_t *scales_bytes) {
+  if (!codes_bytes || !scales_bytes || rows < 0 || cols <= 0) return QLORA_ERR_INVALID_ARG;
+  if ((group != 0 && group != kInt8Group) || cols % 16 != 0 || rows > 0x7fffffff || cols > 0x7fffffff)
+    return QLORA_ERR_UNSUPPORTED;
+  const int64_t groups = group == 0 ? 1 : (cols + kInt8Group - 1) / kInt8Group;
+  *codes_bytes = static_cast<size_t>(rows) * static_cast<size_t>(cols);
+  *scales_bytes = static_cast<size_t>(rows) * static_cast<size_t>(groups) * 4;
+  return QLORA_OK;
+}
+
+static qlora_status check_int8(const qlora_int8_matrix *m) {
+  if (!m || m->rows < 0 || m->cols <= 0 || (m->rows > 0 && (!m->codes || !m->scales))) return QLORA_ERR_INVALID_ARG;
+  if ((m->group != 0 && m->group != kInt8Group) || m->cols % 16 != 0 || m->rows > 0x7fffffff || m->cols > 0x7fffffff)
+    return QLORA_ERR_UNSUPPORTED;
+  if (!aligned16(m->codes) || !aligned16(m->scales)) return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
+
+static qlora_status run_quantize_int8(const void *x, int64_t rows, int64_t cols, int group, int8_t *codes,
+                                      float *scales, cudaStream_t st) {
+  const double n = static_cast<double>(rows) * cols;
+  const double groups = group == 0 ? 1.0 : static_cast<double>((cols + kInt8Group - 1) / kInt8Group);
+  TraceScope ts(K_QUANTIZE_INT8, 0.0, 3.0 * n + 4.0 * rows * groups, st);
+  return launch_quantize_int8(static_cast<const uint16_t *>(x), rows, cols, group, codes, scales, st,
+                              g_trace.recs == nullptr) == cudaSuccess
+             ? QLORA_OK
+             : QLORA_ERR_CUDA;
+}
+
+qlora_status qlora_quantize_int8(const void *x_bf16, int64_t rows, int64_t cols, int32_t group,
+                                 qlora_int8_matrix *out, void *stream) {
+  if (!out || rows < 0 || cols <= 0 || (rows > 0 && !x_bf16)) return QLORA_ERR_INVALID_ARG;
+  qlora_int8_matrix m = *out;
+  m.rows = rows;
+  m.cols = cols;
+  m.group = group;
+  qlora_status cs = check_int8(&m);
+  if (cs != QLORA_OK) return cs;
+  if (!aligned16(x_bf16)) return QLORA_ERR_MISALIGNED;
+  *out = m;
+  if (rows == 0) return QLORA_OK;
+  return run_quantize_int8(x_bf16, rows, cols, group, m.codes, m.scales, static_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *out_bf16, void *stream) {
+  qlora_status cs = check_int8(m);
+  if (cs != QLORA_OK) return cs;
+  if (m->rows == 0) return QLORA_OK;
+  if (!out_bf16) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(out_bf16)) return QLORA_ERR_MISALIGNED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const double n = static_cast<double>(m->rows) * m->cols;
+  const double groups = m->group == 0 ? 1.0 : static_cast<double>((m->cols + kInt8Group - 1) / kInt8Group);
+  TraceScope ts(K_DEQUANTIZE_INT8, 0.0, 3.0 * n + 4.0 * m->rows * groups, st);
+  return launch_dequantize_int8(m->codes, m->scales, m->rows, m->cols, m->group, static_cast<uint16_t *>(out_bf16), st,
+                                g_trace.recs == nullptr) == cudaSuccess
+             ? QLORA_OK
+             : QLORA_ERR_CUDA;
+}
+
+// Checks of both int8 products: the weight, the token count and the output.
+static qlora_status check_linear_int8(int64_t T, int64_t K, const qlora_int8_matrix *w, const void *y,
+                                      const void *status) {
+  qlora_status cs = check_int8(w);
+  if (cs != QLORA_OK) return cs;
+  if (T < 0 || w->rows <= 0 || w->cols != K || (T > 0 && !y)) return QLORA_ERR_INVALID_ARG;
+  // INT32 sums of K products of at most 127 x 127; Y's rows start on 16 bytes
+  if (w->group != 0 || w->rows % 8 != 0 || K > QLORA_INT8_MAX_K || T > QLORA_INT8_MAX_T) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned16(y) || (reinterpret_cast<uintptr_t>(status) & 3u)) return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
+
+// The prepared product (T > 0): xq and sx may still be written by the
+// quantizer that precedes it (early).
+struct Int8Launch {
+  Int8GemmGeom g;
+  Int8GemmArgs a;
+  CUtensorMap m_w, m_x;
+};
+
+static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, const qlora_int8_matrix *w, void *y,
+                                 void *status, bool early, Int8Launch &l) {
+  const int64_t N = w->rows, K = w->cols;
+  l.g = int8_gemm_geom(T, N, K);
+  memset(&l.a, 0, sizeof(l.a));
+  l.a.T = T;
+  l.a.N = N;
+  l.a.K = K;
+  l.a.sx = sx;
+  l.a.sw = w->scales;
+  l.a.y = static_cast<uint16_t *>(y);
+  l.a.stages = l.g.stages;
+  l.a.kb_per_split = l.g.kb_per_split;
+  l.a.early = early && g_trace.recs == nullptr ? 1 : 0;
+  l.a.status = static_cast<uint32_t *>(status);
+  if (!make_map_u8(&l.m_w, w->codes, N, K, K, 128, 128) || !make_map_u8(&l.m_x, xq, T, K, K, l.g.nt, 128))
+    return QLORA_ERR_CUDA;
+  return QLORA_OK;
+}
+
+static qlora_status launch_int8(const Int8Launch &l, cudaStream_t st) {
+  const double T = static_cast<double>(l.a.T), N = static_cast<double>(l.a.N), K = static_cast<double>(l.a.K);
+  TraceScope ts(K_INT8_GEMM, 2.0 * T * N * K, T * K + N * K + 4.0 * (T + N) + 2.0 * T * N, st);
+  return launch_int8_gemm(l.a, l.g, l.m_w, l.m_x, st, g_trace.recs == nullptr) == cudaSuccess ? QLORA_OK
+                                                                                              : QLORA_ERR_CUDA;
+}
+
+size_t qlora_linear_int8_scratch_bytes(int64_t T, int64_t K) {
+  if (T < 0 || T > QLORA_INT8_MAX_T || K <= 0 || K > QLORA_INT8_MAX_K || K % 16 != 0) return 0;
+  return static_cast<size_t>(round_up(T * K, 256) + round_up(T * 4, 256));
+}
+
+qlora_status qlora_linear_int8(const void *x_bf16, int64_t T, const qlora_int8_matrix *w, void *y, void *scratch,
+                               size_t scratch_bytes, void *status, void *stream) {
+  qlora_status cs = check_linear_int8(T, w ? w->cols : 0, w, y, status);
+  if (cs != QLORA_OK) return cs;
+  if (T == 0) return QLORA_OK;
+  if (!x_bf16) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(x_bf16)) return QLORA_ERR_MISALIGNED;
+  const int64_t K = w->cols;
+  if (!scratch || !aligned16(scratch) || scratch_bytes < qlora_linear_int8_scratch_bytes(T, K))
+    return QLORA_ERR_WORKSPACE;
+  int8_t *xq = static_cast<int8_t *>(scratch);
+  float *sx = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + round_up(T * K, 256));
+  Int8Launch l;
+  cs = prepare_int8(xq, sx, T, w, y, status, true, l);
+  if (cs != QLORA_OK) return cs;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cs = run_quantize_int8(x_bf16, T, K, 0, xq, sx, st);
+  if (cs != QLORA_OK) return cs;
+  return launch_int8(l, st);
+}
+
+qlora_status qlora_linear_int8_q(const qlora_int8_matrix *x, const qlora_int8_matrix *w, void *y, void *status,
+                                 void *stream) {
+  qlora_status cs = check_int8(x);
+  if (cs != QLORA_OK) return cs;
+  cs = check_linear_int8(x->rows, x->cols, w, y, status);
+  if (cs != QLORA_OK) return cs;
+  if (x->group != 0) return QLORA_ERR_UNSUPPORTED;   // the product takes one scale a token
+  if (x->rows == 0) return QLORA_OK;
+  Int8Launch l;
+  cs = prepare_int8(x->codes, x->scales, x->rows, w, y, status, false, l);
+  if (cs != QLORA_OK) return cs;
+  return launch_int8(l, static_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_linear_bwd_saved_int8(const void *dy, const qlora_int8_matrix *x, const qlora_nf4_weight *qw,
+                                         const void *A, const void *B, int32_t r, float s, const void *u_saved,
+                                         void *dx, void *dA, void *dB, void *ws, size_t ws_bytes, void *status,
+                                         void *stream) {
+  qlora_status cs = check_int8(x);
+  if (cs != QLORA_OK) return cs;
+  const int64_t T = x->rows;
+  cs = check_linear(x->codes, T, qw, A, B, r, s);
+  if (cs != QLORA_OK) return cs;
+  if (x->cols != qw->cols || (T > 0 && (!dy || !dx || !u_saved)) || !dA || !dB) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(dx) || !aligned16(dA) || !aligned16(dB) || !aligned16(u_saved) ||
+      (reinterpret_cast<uintptr_t>(status) & 3u))
+    return QLORA_ERR_MISALIGNED;
+  const int64_t N = qw->rows, K = qw->cols;
+  if (!ws_ok(ws, ws_bytes, QLORA_OP_BWD, T, N, K, r)) return QLORA_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (cudaMemsetAsync(dA, 0, static_cast<size_t>(r) * K * 2, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    if (cudaMemsetAsync(dB, 0, static_cast<size_t>(N) * r * 2, st) != cudaSuccess) return QLORA_ERR_CUDA;
+    return QLORA_OK;
+  }
+  return linear_bwd_impl(dy, nullptr, x, T, qw, A, B, r, s, u_saved, dx, dA, dB, ws, static_cast<uint32_t *>(status),
+                         st);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,405 @@
+// da_int8.cu -- the adapter gradient dA from an activation kept in 8 bits
+// ("QLoRA: Efficient Fine-Tuning", Step 4 eq. 5, x "cached from the forward
+// pass", here as signed codes with FP32 scales):
+//
+//   dA[j, k] = sum_t dU[t, j] scale[t, g(k)] code[t, k]
+//
+// g(k) = k / 128 (one scale per 128 features of a token) or 0 (one per token).
+// A CTA owns 128 features, so it sees one scale per token either way, and the
+// scale moves to the small operand: dU'[t, j] = dU[t, j] scale[t], while the
+// codes, integers of at most 7 bits and a sign, are exact in BF16.  The product
+// then runs on tcgen05.mma kind::f16 with nothing of the activation rounded.
+// dU arrives as its hi and lo planes; (hi + lo) scale is split again into a hi
+// and a lo plane (about 16 significant bits), two MMAs into one accumulator.
+//
+// Per 64-token stage: TMA brings the codes [64 t][128 k] and the dU^T planes
+// [nb j][64 t]; eight warps turn the codes into the MN-major, 128-byte swizzled
+// BF16 tile the MMA reads (two boxes of 64 features) and the planes into the
+// scaled planes; one thread issues the MMAs.  The tokens are split over the
+// CTAs of a cluster, which sum their FP32 tiles in split order through
+// distributed shared memory.
+//
+// Launched after the dX GEMM as a programmatic dependent whose inputs were all
+// complete before that GEMM started: it runs on the SMs the GEMM's last round
+// leaves idle and waits for it only before it exits.
+//
+// Warps: 0 TMA producer, 1 tensor-memory allocation + MMA issue, 2-9
+// conversion; 2-5 also the epilogue.
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "kernels.h"
+
+namespace qlora {
+
+using namespace gemm;
+
+namespace {
+
+constexpr int AM = 128;                       // features per CTA (MMA M)
+constexpr int AT = 64;                        // tokens per stage
+constexpr int RAW_X = AT * AM;                // 8 KiB of codes
+constexpr int CONV_X = AT * AM * 2;           // 16 KiB: two boxes [64 t][64 k]
+constexpr int kConvStages = 2;
+constexpr int kMaxRaw = 6;
+constexpr int kConvWarps = 8;
+constexpr int kConvThreads = 32 * kConvWarps;
+constexpr int kThreads = 64 + kConvThreads;
+// raw full/empty, conv full/empty, accumulator, tensor-memory slot
+constexpr int kBarBytes = 8 * (2 * kMaxRaw + 2 * kConvStages + 1) + 8;
+constexpr int kFixed = kBarBytes + 1024;
+constexpr int kPitch = AM + 4;
+constexpr int kMaxSmem = 220 * 1024;
+constexpr int kMaxSplits = 8;
+
+int raw_stage_bytes(int nb) { return RAW_X + 2 * nb * AT * 2; }
+int conv_stage_bytes(int nb) { return CONV_X + 2 * nb * AT * 2; }
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_dsmem_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+// Two signed bytes of `w` -> two BF16, exact.  0x4300 | b reads as 128 + b for
+// b < 128 and as 256 + 2 (b - 128) above; with its bit 7 moved to a second
+// operand, code = (128 + (b & 127)) - (128 or 256), one packed subtraction.
+__device__ __forceinline__ uint32_t bytes_to_bf16x2(uint32_t w, uint32_t sel) {
+  const uint32_t v = prmt(w, 0x43434343u, sel);
+  const uint32_t p = v & 0xFF7FFF7Fu, m = v & 0xFF80FF80u;
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&p),
+                                   *reinterpret_cast<const __nv_bfloat162 *>(&m));
+  return *reinterpret_cast<const uint32_t *>(&d);
+}
+
+}  // namespace
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    da_int8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_hi,
+                   const __grid_constant__ CUtensorMap tm_lo, const DaInt8Args a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  constexpr uint32_t Q_BYTES = NB * AT * 2;                  // one plane [NB j][64 t]
+  constexpr uint32_t RAW = RAW_X + 2 * Q_BYTES, CONV = CONV_X + 2 * Q_BYTES;
+  constexpr uint32_t TMEM_COLS = NB < 32 ? 32u : static_cast<uint32_t>(NB);
+  constexpr int CW = NB < 32 ? 16 : 32;
+  constexpr int Q_ITEMS = NB * 8;                            // (j, 8-token chunk) pairs of a stage
+  constexpr int Q_ITER = (Q_ITEMS + kConvThreads - 1) / kConvThreads;
+  const int NR = a.raw_stages;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t raw0 = base + kConvStages * CONV;
+  const uint32_t bar0 = raw0 + static_cast<uint32_t>(NR) * RAW;
+  // the swizzled planes of a stage come first: whole 1 KiB atoms
+  auto raw_q = [&](int s, int p) { return raw0 + static_cast<uint32_t>(s) * RAW + static_cast<uint32_t>(p) * Q_BYTES; };
+  auto raw_x = [&](int s) { return raw0 + static_cast<uint32_t>(s) * RAW + 2 * Q_BYTES; };
+  auto conv_x = [&](int s) { return base + static_cast<uint32_t>(s) * CONV; };
+  auto conv_q = [&](int s, int p) {
+    return base + static_cast<uint32_t>(s) * CONV + CONV_X + static_cast<uint32_t>(p) * Q_BYTES;
+  };
+  auto rfull = [&](int s) { return bar0 + 8u * s; };
+  auto rempty = [&](int s) { return bar0 + 8u * (kMaxRaw + s); };
+  auto cfull = [&](int s) { return bar0 + 8u * (2 * kMaxRaw + s); };
+  auto cempty = [&](int s) { return bar0 + 8u * (2 * kMaxRaw + kConvStages + s); };
+  const uint32_t acc_bar = bar0 + 8u * (2 * kMaxRaw + 2 * kConvStages);
+  const uint32_t tmem_slot = acc_bar + 8;
+  __shared__ volatile int s_abort;
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+  const int splits = static_cast<int>(gridDim.y), split = static_cast<int>(blockIdx.y);
+  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * AM;
+  const int64_t tbeg = static_cast<int64_t>(split) * a.t_per_split;
+  const int64_t tend = min(a.T, tbeg + a.t_per_split);
+  const int nst = static_cast<int>((tend - tbeg + AT - 1) / AT);
+
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(rfull(s), 1);
+      mbar_init(rempty(s), kConvWarps);
+    }
+    for (int s = 0; s < kConvStages; ++s) {
+      mbar_init(cfull(s), kConvWarps);
+      mbar_init(cempty(s), 1);
+    }
+    mbar_init(acc_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_hi);
+    tma_prefetch_desc(&tm_lo);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ld_shared_u32(tmem_slot);
+  grid_dep_launch();
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      int issued = 0;
+      for (int st = 0; st < nst; ++st) {
+        const int s = st % NR;
+        if (s_abort || !mbar_wait(rempty(s), ((st / NR) & 1) ^ 1, a.status)) {
+          s_abort = 1;
+          break;
+        }
+        const int32_t t = static_cast<int32_t>(tbeg + static_cast<int64_t>(st) * AT);
+        mbar_arrive_expect_tx(rfull(s), RAW);
+        tma_load_2d(raw_x(s), &tm_x, rfull(s), static_cast<int32_t>(k0), t);   // [64 t][128 k]
+        tma_load_2d(raw_q(s, 0), &tm_hi, rfull(s), t, 0);                      // [NB j][64 t]
+        tma_load_2d(raw_q(s, 1), &tm_lo, rfull(s), t, 0);
+        issued = st + 1;
+      }
+      if (s_abort)
+        for (int st = max(0, issued - NR); st < issued; ++st) mbar_wait(rfull(st % NR), (st / NR) & 1, a.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issue ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(AM, NB, true, false);
+      bool ok = true;
+      for (int st = 0; st < nst; ++st) {
+        const int s = st % kConvStages;
+        if (!mbar_wait(cfull(s), (st / kConvStages) & 1, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t ad = smem_desc_sw128(conv_x(s) + kk * 2048, CONV_X / 2, 1024);
+          for (int p = 0; p < 2; ++p)
+            tc_mma_ss(tmem, ad, smem_desc_sw128(conv_q(s, p) + kk * 32, 16, 1024), idesc,
+                      (st > 0 || kk > 0 || p > 0) ? 1u : 0u);
+        }
+        tc_commit(cempty(s));
+      }
+      if (!ok) s_abort = 1;
+      tc_commit(acc_bar);   // also drains: arrives once everything issued has completed
+    }
+    __syncwarp();
+  } else {
+    // ---------------- conversion ----------------
+    const int ct = static_cast<int>(threadIdx.x) - 64;
+    const float *sg = a.scales + (a.grouped ? static_cast<int64_t>(blockIdx.x) * a.T : 0);
+    const int ch = ct & 7;   // this thread's 8-token chunk of the planes
+    const bool has_q = ct < Q_ITEMS;
+    float sc[8];
+    auto load_scales = [&](int st) {
+      const int64_t t = tbeg + static_cast<int64_t>(st) * AT + ch * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sc[e] = has_q && st < nst && t + e < tend ? __ldg(sg + t + e) : 0.f;
+    };
+    load_scales(0);
+    for (int st = 0; st < nst; ++st) {
+      const int rs = st % NR, cs = st % kConvStages;
+      bool ok = !s_abort && mbar_wait(rfull(rs), (st / NR) & 1, a.status);
+      ok = ok && mbar_wait(cempty(cs), ((st / kConvStages) & 1) ^ 1, a.status);
+      if (!__all_sync(0xffffffffu, ok)) {
+        s_abort = 1;
+        break;
+      }
+      // the codes: 16 features of one token per item
+#pragma unroll
+      for (int i = 0; i < AT * 8 / kConvThreads; ++i) {
+        const int it = i * kConvThreads + ct;
+        const int t = it >> 3, c16 = it & 7;
+        const uint4 q = ld_shared_v4(raw_x(rs) + static_cast<uint32_t>(t * 128) + (static_cast<uint32_t>(c16 ^ (t & 7)) << 4));
+        const int h = c16 >> 2;   // box of 64 features
+        const uint32_t row = conv_x(cs) + static_cast<uint32_t>(h * (CONV_X / 2) + t * 128);
+        const uint32_t lo[4] = {bytes_to_bf16x2(q.x, 0x4140u), bytes_to_bf16x2(q.x, 0x4342u),
+                                bytes_to_bf16x2(q.y, 0x4140u), bytes_to_bf16x2(q.y, 0x4342u)};
+        const uint32_t hi[4] = {bytes_to_bf16x2(q.z, 0x4140u), bytes_to_bf16x2(q.z, 0x4342u),
+                                bytes_to_bf16x2(q.w, 0x4140u), bytes_to_bf16x2(q.w, 0x4342u)};
+        const uint32_t c = static_cast<uint32_t>((c16 & 3) * 2), x = static_cast<uint32_t>(t & 7);
+        // the two boxes write their two chunks in opposite order: eight lanes
+        // of a token then cover eight different 16-byte bank groups
+        if (h == 0) {
+          st_shared_v4(row + ((c ^ x) << 4), lo[0], lo[1], lo[2], lo[3]);
+          st_shared_v4(row + (((c + 1) ^ x) << 4), hi[0], hi[1], hi[2], hi[3]);
+        } else {
+          st_shared_v4(row + (((c + 1) ^ x) << 4), hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(row + ((c ^ x) << 4), lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      // the planes: eight tokens of one column j per item
+#pragma unroll
+      for (int i = 0; i < Q_ITER; ++i) {
+        const int it = i * kConvThreads + ct;
+        if (it < Q_ITEMS) {
+          const int j = it >> 3;
+          const uint32_t off = static_cast<uint32_t>(j * 128) + ((static_cast<uint32_t>(ch) ^ (j & 7u)) << 4);
+          const uint4 hv = ld_shared_v4(raw_q(rs, 0) + off), lv = ld_shared_v4(raw_q(rs, 1) + off);
+          const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w};
+          uint32_t oh[4], ol[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v0 = (__uint_as_float(hw[e] << 16) + __uint_as_float(lw[e] << 16)) * sc[2 * e];
+            const float v1 = (__uint_as_float(hw[e] & 0xFFFF0000u) + __uint_as_float(lw[e] & 0xFFFF0000u)) * sc[2 * e + 1];
+            const __nv_bfloat162 hh = __floats2bfloat162_rn(v0, v1);
+            oh[e] = *reinterpret_cast<const uint32_t *>(&hh);
+            ol[e] = pack_bf16x2(v0 - __low2float(hh), v1 - __high2float(hh));
+          }
+          st_shared_v4(conv_q(cs, 0) + off, oh[0], oh[1], oh[2], oh[3]);
+          st_shared_v4(conv_q(cs, 1) + off, ol[0], ol[1], ol[2], ol[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(rempty(rs));
+        mbar_arrive(cfull(cs));
+      }
+      load_scales(st + 1);
+    }
+    if (warp < 6) {
+      // ---------------- the FP32 tile to shared memory, column j by column j ----------------
+      const int q = warp & 3;
+      const int row = q * 32 + static_cast<int>(lane);
+      const bool fail = !mbar_wait(acc_bar, 0, a.status) || s_abort;
+      const bool have = __all_sync(0xffffffffu, !fail);   // tcgen05.ld is warp-collective
+      tc_fence_after();
+      // (every warp has left the conversion loop: the accumulator is complete
+      // only after the last conversion, and the ring is drained)
+      const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int c0 = 0; c0 < a.R; c0 += CW) {
+        uint32_t v[CW];
+        if (have) {
+          if constexpr (CW == 16) tmem_ld_32x32b_x16(trow + c0, v);
+          else tmem_ld_32x32b_x32(trow + c0, v);
+          tc_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < CW; ++j) v[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < CW; ++j)
+          if (c0 + j < a.R)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + static_cast<uint32_t>((c0 + j) * kPitch + row) * 4u),
+                         "r"(v[j])
+                         : "memory");
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (splits > 1) cluster_arrive_wait();
+  else __syncthreads();
+  const int items = a.R * (AM / 4);
+  for (int i = split * kThreads + static_cast<int>(threadIdx.x); i < items; i += splits * kThreads) {
+    const int j = i >> 5, f = (i & 31) * 4;
+    const uint32_t local = base + static_cast<uint32_t>(j * kPitch + f) * 4u;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < splits; ++k) {   // split order: the sum does not depend on timing
+      const float4 p = ld_dsmem_f4(mapa_shared(local, static_cast<uint32_t>(k)));
+      s.x += p.x;
+      s.y += p.y;
+      s.z += p.z;
+      s.w += p.w;
+    }
+    if (k0 + f < a.K)   // K % 64 == 0
+      *reinterpret_cast<uint2 *>(a.dA + static_cast<int64_t>(j) * a.K + k0 + f) =
+          make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
+  __syncwarp();
+  // no CTA leaves (and frees its shared memory) while another still reads it
+  if (splits > 1) cluster_arrive_wait();
+  else __syncthreads();
+  grid_dep_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+DaInt8Geom da_int8_geom(int64_t T, int64_t K, int r, int num_sms) {
+  DaInt8Geom g;
+  g.nb = r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
+  const int conv = kConvStages * conv_stage_bytes(g.nb) + kFixed;
+  int per_sm = 2;
+  g.raw_stages = (kMaxSmem / 2 - conv) / raw_stage_bytes(g.nb);
+  if (g.raw_stages < 3) {
+    per_sm = 1;
+    g.raw_stages = (kMaxSmem - conv) / raw_stage_bytes(g.nb);
+  }
+  if (g.raw_stages > kMaxRaw) g.raw_stages = kMaxRaw;
+  g.smem = conv + g.raw_stages * raw_stage_bytes(g.nb);
+  const int64_t tiles = (K + AM - 1) / AM, steps = (T + AT - 1) / AT;
+  int64_t s = static_cast<int64_t>(per_sm) * num_sms / tiles;
+  if (s > kMaxSplits) s = kMaxSplits;
+  if (s > (steps + 1) / 2) s = (steps + 1) / 2;   // at least two stages a split
+  if (s < 1) s = 1;
+  g.t_per_split = (steps + s - 1) / s * AT;
+  g.splits = static_cast<int>((T + g.t_per_split - 1) / g.t_per_split);
+  return g;
+}
+
+namespace {
+template <int NB>
+cudaError_t launch_nb(const DaInt8Args &a, const DaInt8Geom &g, const CUtensorMap &tm_x, const CUtensorMap &tm_hi,
+                      const CUtensorMap &tm_lo, cudaStream_t st, bool pdl) {
+  const int ring = kConvStages * conv_stage_bytes(NB) + g.raw_stages * raw_stage_bytes(NB);
+  if (g.smem != ring + kFixed || g.smem > kMaxSmem || ring < a.R * kPitch * 4 || a.R > NB) return cudaErrorInvalidValue;
+  cudaError_t e = ensure_smem_optin(reinterpret_cast<const void *>(da_int8_kernel<NB>), kMaxSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.K + AM - 1) / AM), static_cast<unsigned>(g.splits), 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(g.smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  if (g.splits > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = 1;
+    attr[na].val.clusterDim.y = static_cast<unsigned>(g.splits);
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  if (pdl) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  return cudaLaunchKernelEx(&cfg, da_int8_kernel<NB>, tm_x, tm_hi, tm_lo, a);
+}
+}  // namespace
+
+cudaError_t launch_da_int8(const DaInt8Args &a, const DaInt8Geom &g, const CUtensorMap &tm_x,
+                           const CUtensorMap &tm_du_hi, const CUtensorMap &tm_du_lo, cudaStream_t st, bool pdl) {
+  if (a.T <= 0 || a.K <= 0 || a.K % 64 != 0 || a.R < 1 || g.raw_stages < 1 || g.raw_stages > kMaxRaw ||
+      g.splits < 1 || g.splits > kMaxSplits)
+    return cudaErrorInvalidValue;
+  if (a.raw_stages != g.raw_stages || a.t_per_split != g.t_per_split || g.t_per_split % AT != 0 ||
+      g.splits != (a.T + g.t_per_split - 1) / g.t_per_split)
+    return cudaErrorInvalidValue;
+  switch (g.nb) {
+    case 16: return launch_nb<16>(a, g, tm_x, tm_du_hi, tm_du_lo, st, pdl);
+    case 32: return launch_nb<32>(a, g, tm_x, tm_du_hi, tm_du_lo, st, pdl);
+    case 64: return launch_nb<64>(a, g, tm_x, tm_du_hi, tm_du_lo, st, pdl);
+    case 128: return launch_nb<128>(a, g, tm_x, tm_du_hi, tm_du_lo, st, pdl);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace qlora

@@ -1,0 +1,269 @@
+// int8.cu -- the 8-bit row format: quantization of a BF16 matrix to signed
+// 8-bit codes with one FP32 scale per row or per 128 consecutive columns of a
+// row, and its dequantization.
+//
+//   amax  = max |x| over the group
+//   scale = max(RN32(amax / 127), 2^-126),  inv = RN32(1 / scale)
+//   code  = RNE_int(x inv), the exact product rounded once
+//   value = code * scale
+//
+// The exact product needs no second rounding: fma(x, inv, 1.5 * 2^23) rounds
+// x inv + 1.5 * 2^23 to an integer (ulp 1 there), ties to even, and leaves the
+// code as the two's complement low byte of the sum.  |x| inv <= 127 (1 + 2^-23),
+// so no code leaves [-127, 127].  The floor of 2^-126 keeps inv finite for rows
+// of subnormals and zeros.  A group that holds an infinity or a NaN gets scale
+// NaN and codes 0: whatever is computed from it is NaN, never a wrong number.
+//
+// Inputs are read with coherent loads after griddepcontrol.wait: the kernel
+// before may still have been writing them when this one started.
+//
+// Both kernels move each byte once (2 + 1 bytes an element in, 1 + 2 out):
+// bound by HBM for large matrices, by launch latency for a few rows.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace qlora {
+
+namespace {
+
+constexpr float kRoundMagic = 12582912.0f;   // 1.5 * 2^23
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
+
+// elementwise max over |bits| of eight BF16 values (BF16 order = magnitude order), as u16x2
+__device__ __forceinline__ uint32_t abs_max8(const uint4 &v) {
+  return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+}
+
+__device__ __forceinline__ uint32_t fold_u16x2(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+
+struct RowScale {
+  float scale, inv;
+  bool bad;
+};
+
+__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
+  RowScale r;
+  r.bad = amax_bits >= 0x7F80u;
+  const float s = fmaxf(__fdiv_rn(__uint_as_float(amax_bits << 16), 127.0f), kMinScale);
+  r.scale = r.bad ? __uint_as_float(0x7FC00000u) : s;
+  r.inv = __frcp_rn(s);
+  return r;
+}
+
+// two BF16 values of a word -> the sums whose low bytes are their codes
+__device__ __forceinline__ uint32_t code_lo(uint32_t w, float inv) {
+  return __float_as_uint(__fmaf_rn(__uint_as_float(w << 16), inv, kRoundMagic));
+}
+__device__ __forceinline__ uint32_t code_hi(uint32_t w, float inv) {
+  return __float_as_uint(__fmaf_rn(__uint_as_float(w & 0xFFFF0000u), inv, kRoundMagic));
+}
+
+__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float inv) {
+  const uint32_t a = prmt(code_lo(w0, inv), code_hi(w0, inv), 0x0040);
+  const uint32_t b = prmt(code_lo(w1, inv), code_hi(w1, inv), 0x0040);
+  return prmt(a, b, 0x5410);
+}
+
+__device__ __forceinline__ uint2 codes8(const uint4 &v, const RowScale &r) {
+  if (r.bad) return make_uint2(0u, 0u);
+  return make_uint2(codes4(v.x, v.y, r.inv), codes4(v.z, v.w, r.inv));
+}
+
+// One scale a row.  A row is held in registers by THREADS threads, VPT 16-byte
+// loads each, so it is read once; the maximum crosses the warps of the row
+// through shared memory.  ROWS rows share a CTA when a row is one warp.
+template <int THREADS, int VPT, int ROWS>
+__global__ void __launch_bounds__(THREADS *ROWS) quantize_rows_kernel(const uint4 *__restrict__ x, int64_t rows,
+                                                                      int vecs, uint2 *__restrict__ codes,
+                                                                      float *__restrict__ scales) {
+  static_assert(ROWS == 1 || THREADS == 32, "rows share a CTA only one warp each");
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = ROWS == 1 ? threadIdx.x : threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + (ROWS == 1 ? 0 : threadIdx.x >> 5);
+  if (row >= rows) return;   // (whole warps: ROWS > 1 only)
+  const uint4 *src = x + row * vecs;
+  uint4 v[VPT];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * THREADS + tid;
+    v[i] = c < vecs ? __ldcg(src + c) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) m = __vmaxu2(m, abs_max8(v[i]));
+  uint32_t a = __reduce_max_sync(0xffffffffu, fold_u16x2(m));
+  if constexpr (THREADS > 32) {
+    __shared__ uint32_t s_max[THREADS / 32];
+    if ((tid & 31) == 0) s_max[tid >> 5] = a;
+    __syncthreads();
+    a = (tid & 31) < THREADS / 32 ? s_max[tid & 31] : 0u;
+    a = __reduce_max_sync(0xffffffffu, a);
+  }
+  const RowScale r = row_scale(a);
+  if (tid == 0) scales[row] = r.scale;
+  uint2 *dst = codes + row * vecs;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * THREADS + tid;
+    if (c < vecs) dst[c] = codes8(v[i], r);
+  }
+}
+
+// Rows longer than the registers of a CTA: the row is read twice (the second
+// read hits L2).
+__global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const uint4 *__restrict__ x, int64_t vecs,
+                                                                  uint2 *__restrict__ codes,
+                                                                  float *__restrict__ scales) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ uint32_t s_max[32];
+  const int64_t row = blockIdx.x;
+  const uint4 *src = x + row * vecs;
+  uint32_t m = 0;
+  for (int64_t c = threadIdx.x; c < vecs; c += 1024) m = __vmaxu2(m, abs_max8(__ldcg(src + c)));
+  uint32_t a = __reduce_max_sync(0xffffffffu, fold_u16x2(m));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = __reduce_max_sync(0xffffffffu, s_max[threadIdx.x & 31]);
+  const RowScale r = row_scale(a);
+  if (threadIdx.x == 0) scales[row] = r.scale;
+  uint2 *dst = codes + row * vecs;
+  for (int64_t c = threadIdx.x; c < vecs; c += 1024) dst[c] = codes8(__ldcg(src + c), r);
+}
+
+// One scale per 128 columns of a row: 16 lanes hold a group (8 values each), a
+// warp two neighbouring groups of kGroupRows rows, whose loads are in flight
+// together.  Scales are stored group by group, [groups][rows], so that the
+// kGroupRows scales of a group are one 32-byte sector.
+constexpr int kGroupRows = 8;
+constexpr int kGroupWarps = 4;
+
+__global__ void __launch_bounds__(32 * kGroupWarps)
+    quantize_groups_kernel(const uint4 *__restrict__ x, int64_t rows, int vecs, int groups, int pairs,
+                           uint2 *__restrict__ codes, float *__restrict__ scales) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kGroupWarps + (threadIdx.x >> 5);
+  const int64_t slab = unit / pairs;
+  const int64_t row0 = slab * kGroupRows;
+  if (row0 >= rows) return;
+  const int pair = static_cast<int>(unit - slab * pairs);
+  const int c = pair * 32 + lane;
+  const bool in = c < vecs;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kGroupRows), rows - row0));
+  uint4 v[kGroupRows];
+#pragma unroll
+  for (int i = 0; i < kGroupRows; ++i)
+    v[i] = in && i < n ? __ldcg(x + (row0 + i) * vecs + c) : make_uint4(0, 0, 0, 0);
+  float mine = 0.f;
+#pragma unroll
+  for (int i = 0; i < kGroupRows; ++i) {
+    uint32_t m = fold_u16x2(abs_max8(v[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const RowScale r = row_scale(m);
+    if ((lane & 15) == i) mine = r.scale;
+    if (in && i < n) codes[(row0 + i) * vecs + c] = codes8(v[i], r);
+  }
+  const int g = pair * 2 + (lane >> 4);
+  if (g < groups && (lane & 15) < n) scales[static_cast<int64_t>(g) * rows + row0 + (lane & 15)] = mine;
+}
+
+__device__ __forceinline__ uint32_t value2(uint32_t w, int byte, float s) {
+  const float lo = static_cast<float>(static_cast<int8_t>(w >> (8 * byte)));
+  const float hi = static_cast<float>(static_cast<int8_t>(w >> (8 * byte + 8)));
+  return pack_bf16x2(__fmul_rn(lo, s), __fmul_rn(hi, s));
+}
+
+// One thread per 16 codes of a row: BF16_RNE(RN32(code * scale)).
+__global__ void __launch_bounds__(256) dequantize_int8_kernel(const uint4 *__restrict__ codes,
+                                                              const float *__restrict__ scales, int64_t rows, int units,
+                                                              int group_units, uint4 *__restrict__ out) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int u = static_cast<int>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (u >= units) return;
+  const float *sg = scales + (group_units ? static_cast<int64_t>(u / group_units) * rows : 0);
+  for (int64_t row = static_cast<int64_t>(blockIdx.y) * blockDim.y + threadIdx.y; row < rows;
+       row += static_cast<int64_t>(gridDim.y) * blockDim.y) {
+    const uint4 q = __ldcg(codes + row * units + u);
+    const float s = __ldca(sg + row);
+    uint4 *dst = out + 2 * (row * units + u);
+    dst[0] = make_uint4(value2(q.x, 0, s), value2(q.x, 2, s), value2(q.y, 0, s), value2(q.y, 2, s));
+    dst[1] = make_uint4(value2(q.z, 0, s), value2(q.z, 2, s), value2(q.w, 0, s), value2(q.w, 2, s));
+  }
+}
+
+cudaLaunchConfig_t make_cfg(dim3 grid, dim3 block, cudaStream_t st, bool pdl, cudaLaunchAttribute *attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cfg;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_int8(const uint16_t *x, int64_t rows, int64_t cols, int group, int8_t *codes,
+                                 float *scales, cudaStream_t st, bool pdl) {
+  if (rows <= 0) return cudaSuccess;
+  const uint4 *src = reinterpret_cast<const uint4 *>(x);
+  uint2 *dst = reinterpret_cast<uint2 *>(codes);
+  const int64_t vecs = cols / 8;
+  cudaLaunchAttribute attr[1];
+  if (group != 0) {
+    const int groups = static_cast<int>((cols + kInt8Group - 1) / kInt8Group);
+    const int pairs = (groups + 1) / 2;
+    const int64_t units = (rows + kGroupRows - 1) / kGroupRows * pairs;
+    const int64_t blocks = (units + kGroupWarps - 1) / kGroupWarps;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const cudaLaunchConfig_t cfg = make_cfg(dim3(static_cast<unsigned>(blocks)), dim3(32 * kGroupWarps), st, pdl, attr);
+    return cudaLaunchKernelEx(&cfg, quantize_groups_kernel, src, rows, static_cast<int>(vecs), groups, pairs, dst,
+                              scales);
+  }
+  if (rows > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned n = static_cast<unsigned>(rows);
+  const int nv = static_cast<int>(vecs);
+  if (vecs <= 32 * 4) {
+    const cudaLaunchConfig_t cfg = make_cfg(dim3((n + 3) / 4), dim3(128), st, pdl, attr);
+    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<32, 4, 4>, src, rows, nv, dst, scales);
+  }
+  if (vecs <= 128 * 4) {
+    const cudaLaunchConfig_t cfg = make_cfg(dim3(n), dim3(128), st, pdl, attr);
+    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<128, 4, 1>, src, rows, nv, dst, scales);
+  }
+  if (vecs <= 512 * 4) {
+    const cudaLaunchConfig_t cfg = make_cfg(dim3(n), dim3(512), st, pdl, attr);
+    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<512, 4, 1>, src, rows, nv, dst, scales);
+  }
+  if (vecs <= 1024 * 4) {
+    const cudaLaunchConfig_t cfg = make_cfg(dim3(n), dim3(1024), st, pdl, attr);
+    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<1024, 4, 1>, src, rows, nv, dst, scales);
+  }
+  const cudaLaunchConfig_t cfg = make_cfg(dim3(n), dim3(1024), st, pdl, attr);
+  return cudaLaunchKernelEx(&cfg, quantize_long_rows_kernel, src, vecs, dst, scales);
+}
+
+cudaError_t launch_dequantize_int8(const int8_t *codes, const float *scales, int64_t rows, int64_t cols, int group,
+                                   uint16_t *out, cudaStream_t st, bool pdl) {
+  if (rows <= 0) return cudaSuccess;
+  const int64_t units = cols / 16;
+  int bx = 1;
+  while (bx < 256 && bx < units) bx *= 2;
+  const int by = 256 / bx;
+  const int64_t gy = (rows + by - 1) / by;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      make_cfg(dim3(static_cast<unsigned>((units + bx - 1) / bx), static_cast<unsigned>(gy < 65535 ? gy : 65535)),
+               dim3(static_cast<unsigned>(bx), static_cast<unsigned>(by)), st, pdl, attr);
+  return cudaLaunchKernelEx(&cfg, dequantize_int8_kernel, reinterpret_cast<const uint4 *>(codes), scales, rows,
+                            static_cast<int>(units), group / 16, reinterpret_cast<uint4 *>(out));
+}
+
+}  // namespace qlora

@@ -48,6 +48,65 @@ cudaError_t launch_adam(float *param, float *m, float *v, const uint16_t *grad, 
                         const AdamArgs &a, cudaStream_t st, int num_sms);
 
 // ---------------------------------------------------------------------------
+// the 8-bit row format (int8.cu): signed codes [rows][cols], scales
+// [groups][rows], one group a row (group 0) or one per kInt8Group columns
+// ---------------------------------------------------------------------------
+constexpr int kInt8Group = 128;
+// cols a multiple of 16
+cudaError_t launch_quantize_int8(const uint16_t *x, int64_t rows, int64_t cols, int group, int8_t *codes,
+                                 float *scales, cudaStream_t st, bool pdl);
+cudaError_t launch_dequantize_int8(const int8_t *codes, const float *scales, int64_t rows, int64_t cols, int group,
+                                   uint16_t *out, cudaStream_t st, bool pdl);
+
+// ---------------------------------------------------------------------------
+// Y[T, N] = sx[t] sw[n] sum_k Xq[t, k] Wq[n, k] on kind::i8 (int8_gemm.cu)
+// ---------------------------------------------------------------------------
+struct Int8GemmGeom {
+  int nt;               // tokens per tile (the MMA's N): 16, 32, 64, 128 or 256
+  int stages;           // TMA pipeline depth
+  int smem;             // dynamic shared memory bytes
+  int splits;           // contraction splits of a tile: the CTAs of one cluster
+  int kb_per_split;     // 128-byte contraction blocks per split
+};
+Int8GemmGeom int8_gemm_geom(int64_t T, int64_t N, int64_t K);
+struct Int8GemmArgs {
+  int64_t T, N, K;
+  const float *sx, *sw;   // [T], [N]
+  uint16_t *y;            // [T, N] BF16
+  int stages, kb_per_split;
+  int early;              // the preceding kernel wrote only the activations: weights load before the dependency wait
+  uint32_t *status;
+};
+// maps: Wq [N rows, K bytes] box 128 x 128, Xq [T rows, K bytes] box nt x 128, 128-byte swizzle
+cudaError_t launch_int8_gemm(const Int8GemmArgs &a, const Int8GemmGeom &g, const CUtensorMap &tm_w,
+                             const CUtensorMap &tm_x, cudaStream_t st, bool pdl);
+
+// ---------------------------------------------------------------------------
+// dA = dU^T Xq from the 8-bit activation (da_int8.cu)
+// ---------------------------------------------------------------------------
+struct DaInt8Geom {
+  int nb;                // r rounded up to 16, 32, 64 or 128 (the MMA's N)
+  int raw_stages;        // code tiles in flight
+  int smem;              // dynamic shared memory bytes
+  int splits;            // token splits of a 128-feature tile: the CTAs of one cluster
+  int64_t t_per_split;   // multiple of 64
+};
+DaInt8Geom da_int8_geom(int64_t T, int64_t K, int r, int num_sms);
+struct DaInt8Args {
+  int64_t T, K;
+  int R;
+  int raw_stages;
+  int64_t t_per_split;
+  const float *scales;   // [groups][T]
+  int grouped;           // 1: one group per 128 features (a tile), 0: one a row
+  uint16_t *dA;          // [R, K] BF16
+  uint32_t *status;
+};
+// maps: codes [T rows, K bytes] box 64 x 128, 128-byte swizzle; the dU^T planes [R rows, T cols] box nb x 64
+cudaError_t launch_da_int8(const DaInt8Args &a, const DaInt8Geom &g, const CUtensorMap &tm_x,
+                           const CUtensorMap &tm_du_hi, const CUtensorMap &tm_du_lo, cudaStream_t st, bool pdl);
+
+// ---------------------------------------------------------------------------
 // fused NF4 GEMMs on CTA pairs (gemm_fwd_2sm.cu, gemm_dx_2sm.cu)
 // ---------------------------------------------------------------------------
 struct GemmParams {

@@ -336,6 +336,95 @@ QLORA_API qlora_status qlora_linear_fwd_noalloc(const void *x, int64_t T, const 
 QLORA_API qlora_status qlora_noalloc_get_error(void *stream);
 
 /*
+ * A matrix in 8 bits (all buffers on the device, caller-owned): signed codes
+ * with one FP32 scale per row (group = 0) or per 128 consecutive columns of a
+ * row (group = 128, the last group of a row may be short).
+ *   codes   int8[rows*cols], row-major.
+ *   scales  float[groups*rows]: the scale of row i, group g at g * rows + i
+ *           (groups = 1, or ceil(cols / 128)).
+ * Value: code * scale.  Of a group with amax = max |x|:
+ *   scale = max(RN32(amax / 127), 2^-126);  inv = RN32(1 / scale);
+ *   code = the integer nearest to x * inv (the exact product), ties to even.
+ * A group that holds an infinity or a NaN has scale NaN and codes 0, so that
+ * everything computed from it is NaN; it is not reported as an error.
+ * rows >= 0, cols a positive multiple of 16; codes and scales 16-byte aligned.
+ * The pages have no counterpart to the format: it keeps the activation that
+ * eq. 5 takes "cached from the forward pass" in half the memory, and is the
+ * operand format of the int8 product below.
+ */
+typedef struct {
+  int8_t *codes;
+  float *scales;
+  int64_t rows;
+  int64_t cols;
+  int32_t group;       /* 0 or 128 */
+} qlora_int8_matrix;
+
+/* Bytes of both buffers.  Host-only.  Errors: INVALID_ARG (null output, rows
+ * < 0, cols <= 0), UNSUPPORTED (group not 0 or 128, cols % 16 != 0). */
+QLORA_API qlora_status qlora_int8_storage_bytes(int64_t rows, int64_t cols, int32_t group, size_t *codes_bytes,
+                                                size_t *scales_bytes);
+
+/*
+ * Quantize a BF16 matrix x[rows, cols] (16-byte aligned) to the 8-bit format.
+ * `out` supplies the two buffers; the call fills out->rows/cols/group.  Group
+ * 128 keeps the values of a row apart from its outlier channels: use it for
+ * activations kept for the backward; group 0 is what the int8 product takes
+ * (per token, per output channel).  rows == 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA.
+ */
+QLORA_API qlora_status qlora_quantize_int8(const void *x_bf16, int64_t rows, int64_t cols, int32_t group,
+                                           qlora_int8_matrix *out, void *stream);
+
+/* out[rows, cols] (16-byte aligned) = BF16_RNE(RN32(code * scale)). */
+QLORA_API qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *out_bf16, void *stream);
+
+/*
+ * The int8 product of a merged weight (qlora_merge_adapter, then
+ * qlora_quantize_int8 with group 0: one scale per output channel) with
+ * activations quantized per token:
+ *   acc[t, n] = sum_k xq[t, k] wq[n, k] in INT32, exact;
+ *   y[t, n] = BF16_RNE(RN32(RN32(float(acc) * sx[t]) * sw[n])).
+ * qlora_linear_int8 quantizes x[T, K] (BF16) into `scratch` and multiplies;
+ * qlora_linear_int8_q takes an already quantized x (group 0), so that several
+ * products can share one.  y[T, N]: BF16, 16-byte aligned.  Results do not
+ * depend on timing.  N % 8 == 0, K % 16 == 0, K <= QLORA_INT8_MAX_K (the INT32
+ * sums stay exact), T <= QLORA_INT8_MAX_T; T == 0 is a no-op.
+ * scratch: qlora_linear_int8_scratch_bytes(T, K) bytes (0 on invalid
+ * arguments), 16-byte aligned; it need not be initialised and holds nothing
+ * between calls, but calls that may overlap must not share it.
+ * status: a status word as at the start of a workspace (zeroed once, read by
+ * qlora_get_error(status, stream)); any number of calls may share it; NULL: a
+ * bounded wait that runs out is not reported.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
+ */
+#define QLORA_INT8_MAX_K 131072
+#define QLORA_INT8_MAX_T (65535 * 256)
+QLORA_API size_t qlora_linear_int8_scratch_bytes(int64_t T, int64_t K);
+QLORA_API qlora_status qlora_linear_int8(const void *x_bf16, int64_t T, const qlora_int8_matrix *w, void *y,
+                                         void *scratch, size_t scratch_bytes, void *status, void *stream);
+QLORA_API qlora_status qlora_linear_int8_q(const qlora_int8_matrix *x, const qlora_int8_matrix *w, void *y,
+                                           void *status, void *stream);
+
+/*
+ * qlora_linear_bwd_saved with the activation kept in 8 bits: dA = dU^T x with
+ * x the values of `x` (T = x->rows rows of x->cols = K, either group), exactly
+ * as coded (the scales multiply dU, nothing of x is rounded again); dX, dU and
+ * dB as in qlora_linear_bwd_saved, from dy and the saved U.  The forward saves
+ * U (qlora_linear_fwd_save) and the caller quantizes its x
+ * (qlora_quantize_int8); x itself need not be kept, and projections that share
+ * an input share one quantized copy.
+ * ws: qlora_workspace_bytes(QLORA_OP_BWD, T, N, K, r) bytes, 256-byte aligned;
+ * it need not be initialised and holds nothing between calls, but calls that
+ * may overlap must not share it.  status: as in qlora_linear_int8.
+ * Errors: as qlora_linear_bwd_saved, and those of the 8-bit format.
+ */
+QLORA_API qlora_status qlora_linear_bwd_saved_int8(const void *dy, const qlora_int8_matrix *x,
+                                                   const qlora_nf4_weight *qw, const void *A, const void *B, int32_t r,
+                                                   float s, const void *u_saved, void *dx, void *dA, void *dB,
+                                                   void *ws, size_t ws_bytes, void *status, void *stream);
+
+/*
  * Failure-detection self-test (a diagnostic; the pages have no counterpart).
  * Launches one kernel whose thread waits, with the bounded mbarrier wait that
  * every pipeline of the library uses, on a barrier that nothing arrives on;

@@ -391,6 +391,64 @@ def normal_cdf(x: float) -> float:
 
 
 # ----------------------------------------------------------------------------
+# 8 bits: activations kept for eq. 5's "cached from the forward pass", and the
+# product that serves a merged weight.  The pages have no counterpart.
+# ----------------------------------------------------------------------------
+
+INT8_GROUP = 128
+INT8_MIN_SCALE = F32(2.0 ** -126)
+
+
+def quantize_int8(x_bits, group: int = 0):
+    """Signed 8-bit codes [rows, cols] and FP32 scales [groups, rows] of a BF16
+    matrix: one scale per row (group 0) or per `group` columns of a row.
+
+    scale = max(RN32(amax / 127), 2^-126), inv = RN32(1 / scale), code = the
+    integer nearest to x * inv, ties to even (x * inv has at most 8 + 24
+    significant bits: exact in float64).  A group with an infinity or a NaN
+    gets scale NaN and codes 0.
+    """
+    x = bf16_bits_to_f32(x_bits)
+    rows, cols = x.shape
+    g = group or cols
+    codes = np.zeros((rows, cols), np.int8)
+    scales = np.empty((-(-cols // g), rows), F32)
+    for i, c0 in enumerate(range(0, cols, g)):
+        blk = x[:, c0:c0 + g]
+        finite = np.isfinite(blk).all(1)
+        safe = np.where(finite[:, None], blk, F32(0))
+        scale = np.maximum(np.abs(safe).max(1) / F32(127), INT8_MIN_SCALE).astype(F32)
+        inv = (F32(1) / scale).astype(F32)
+        codes[:, c0:c0 + g] = np.rint(safe.astype(F64) * inv.astype(F64)[:, None]).astype(np.int8)
+        scales[i] = np.where(finite, scale, F32(np.nan))
+    return codes, scales
+
+
+def values_int8(codes, scales, group: int = 0):
+    """code * scale in float64, [rows, cols]."""
+    s = np.asarray(scales, F64)
+    cols = codes.shape[1]
+    g = group or cols
+    return codes.astype(F64) * np.repeat(s.T, g, axis=1)[:, :cols]
+
+
+def dequantize_int8(codes, scales, group: int = 0):
+    """BF16_RNE(RN32(code * scale)) as BF16 bits, [rows, cols]."""
+    cols = codes.shape[1]
+    s = np.repeat(np.asarray(scales, F32).T, group or cols, axis=1)[:, :cols]
+    return f32_to_bf16_bits((codes.astype(F32) * s).astype(F32))
+
+
+def linear_int8(xq, sx, wq, sw):
+    """BF16 bits [T, N] of the int8 product: the integer sums (float64 holds
+    them exactly), converted to FP32, then times sx[t], then times sw[n], each
+    step rounded to FP32, the result to BF16."""
+    acc = xq.astype(F64) @ wq.astype(F64).T
+    y = (acc.astype(F32) * np.asarray(sx, F32).reshape(-1, 1)).astype(F32)
+    return f32_to_bf16_bits((y * np.asarray(sw, F32).reshape(1, -1)).astype(F32))
+
+
+# ----------------------------------------------------------------------------
 # The adapters' optimizer step ("What is QLoRA?", "The three pieces": paged
 # optimizers keep the optimizer state in unified memory; "Worked example":
 # adapters in fp32 with gradients and Adam moments, 16 bytes each).
