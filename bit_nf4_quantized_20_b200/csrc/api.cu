@@ -1363,7 +1363,8 @@ static qlora_status check_linear_int8(int64_t T, int64_t K, const qlora_int8_mat
 struct Int8Launch {
   Int8GemmGeom g;
   Int8GemmArgs a;
-  CUtensorMap m_w, m_x;
+  Int8PairArgs p;
+  CUtensorMap m_w, m_x, m_xh, m_y;
 };
 
 static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, const qlora_int8_matrix *w, void *y,
@@ -1371,6 +1372,7 @@ static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, c
   const int64_t N = w->rows, K = w->cols;
   l.g = int8_gemm_geom(T, N, K);
   memset(&l.a, 0, sizeof(l.a));
+  memset(&l.p, 0, sizeof(l.p));
   l.a.T = T;
   l.a.N = N;
   l.a.K = K;
@@ -1381,7 +1383,17 @@ static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, c
   l.a.kb_per_split = l.g.kb_per_split;
   l.a.early = early && g_trace.recs == nullptr ? 1 : 0;
   l.a.status = static_cast<uint32_t *>(status);
-  if (!make_map_u8(&l.m_w, w->codes, N, K, K, 128, 128) || !make_map_u8(&l.m_x, xq, T, K, K, l.g.nt, 128))
+  l.p.T = T;
+  l.p.N = N;
+  l.p.K = K;
+  l.p.sx = l.a.sx;
+  l.p.sw = l.a.sw;
+  l.p.status = l.a.status;
+  l.p.early = l.a.early;
+  if (!make_map_u8(&l.m_w, w->codes, N, K, K, 128, 128) ||
+      !make_map_u8(&l.m_x, xq, T, K, K, l.g.pair ? 128 : l.g.nt, 128))
+    return QLORA_ERR_CUDA;
+  if (l.g.pair && (!make_map_u8(&l.m_xh, xq, T, K, K, 64, 128) || !make_map_bf16(&l.m_y, y, T, N, N, 64, 64, true)))
     return QLORA_ERR_CUDA;
   return QLORA_OK;
 }
@@ -1389,8 +1401,10 @@ static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, c
 static qlora_status launch_int8(const Int8Launch &l, cudaStream_t st) {
   const double T = static_cast<double>(l.a.T), N = static_cast<double>(l.a.N), K = static_cast<double>(l.a.K);
   TraceScope ts(K_INT8_GEMM, 2.0 * T * N * K, T * K + N * K + 4.0 * (T + N) + 2.0 * T * N, st);
-  return launch_int8_gemm(l.a, l.g, l.m_w, l.m_x, st, g_trace.recs == nullptr) == cudaSuccess ? QLORA_OK
-                                                                                              : QLORA_ERR_CUDA;
+  const bool pdl = g_trace.recs == nullptr;
+  const cudaError_t e = l.g.pair ? launch_int8_gemm_2sm(l.p, l.m_w, l.m_x, l.m_xh, l.m_y, num_sms_current(), st, pdl)
+                                 : launch_int8_gemm(l.a, l.g, l.m_w, l.m_x, st, pdl);
+  return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 size_t qlora_linear_int8_scratch_bytes(int64_t T, int64_t K) {

@@ -404,6 +404,19 @@ __device__ __forceinline__ void tc_mma_ss_pair_lo(uint32_t d_tmem, uint32_t a_lo
       : "memory");
 }
 
+// The _ss form for signed 8-bit operands and INT32 accumulators, kind::i8 (K = 32).
+__device__ __forceinline__ void tc_mma_ss_pair_i8_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                                     uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 ad, {%1, %2};\n\t"
+      "mov.b64 bd, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], ad, bd, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive (once each) on the mbarrier at the same offset in every CTA of
 // `cta_mask` when all prior tcgen05 ops of this thread complete.
 __device__ __forceinline__ void tc_commit_pair_mc(uint32_t bar, uint16_t cta_mask) {

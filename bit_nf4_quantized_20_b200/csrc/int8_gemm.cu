@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kThreads)
 
 Int8GemmGeom int8_gemm_geom(int64_t T, int64_t N, int64_t K) {
   Int8GemmGeom g;
+  g.pair = T > 256;
   g.nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
   const int stage = W_BYTES + g.nt * KB;
   g.stages = g.nt <= 32 ? 4 : g.nt <= 128 ? 3 : 4;

@@ -1,0 +1,369 @@
+// int8_gemm_2sm.cu -- the int8 product of int8_gemm.cu for token counts that
+// fill the GPU with 256 x 256 tiles, on CTA pairs:
+//
+//   Y[t, n] = BF16_RNE(RN32(RN32(float(sum_k Xq[t, k] Wq[n, k]) * sx[t]) * sw[n]))
+//
+// A cluster of two CTAs on two SMs owns 256 weight rows x 256 tokens; the even
+// CTA issues tcgen05.mma.cta_group::2.kind::i8 (M = 256, N = 256, K = 32).  Per
+// 128-byte contraction stage each CTA loads its 128 weight rows and 128 tokens
+// by TMA (32 KiB), so an operand byte feeds 256 products; six stages are in
+// flight.  Two 256-column INT32 accumulators in tensor memory let the epilogue
+// of one tile run under the next tile's MMAs: tcgen05.ld, conversion and the
+// two scales, BF16 pairs into a swizzled 64-token staging chunk (two of them in
+// turn), TMA store.
+//
+// Bound by the tensor cores; the tiles run in blocks of eight weight tiles by
+// all token tiles, so that the pairs running at one time share operands in L2.
+// A last round at most half full runs its tiles as 128-token halves.
+//
+// Warps: 0-3 epilogue, 4 TMA, 5 paired tensor-memory allocation and, on the
+// even CTA, the MMA issue.
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "kernels.h"
+
+namespace qlora {
+
+using namespace gemm;
+
+namespace {
+
+constexpr int PM = 128;                        // weight rows per CTA (256 per pair)
+constexpr int PN = 256;                        // tokens per tile
+constexpr int HN = 128;                        // tokens loaded by each CTA
+constexpr int KB = 128;                        // contraction bytes per stage
+constexpr int STAGES = 6;
+constexpr int A_BYTES = PM * KB;               // 16 KiB
+constexpr int B_BYTES = HN * KB;               // 16 KiB
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int CHUNK_T = 64;                    // tokens per staging chunk
+constexpr int BOX_BYTES = CHUNK_T * 128;       // 64 tokens x 64 features, BF16
+constexpr int CHUNK_BYTES = 2 * BOX_BYTES;
+constexpr int kThreads = 192;
+constexpr int kTmemCols = 512;
+constexpr int kGroupM = 8;                     // weight tiles per block of tiles
+constexpr int EPI_BAR = 1, EPI_ANY_BAR = 2;
+
+constexpr int OFF_OUT = STAGES * STAGE_BYTES;
+constexpr int OFF_SX = OFF_OUT + 2 * CHUNK_BYTES;
+constexpr int OFF_BAR = OFF_SX + PN * 4;
+// full[S], empty[S], acc_full[2], acc_empty[2], drain
+constexpr int NUM_BARS = 2 * STAGES + 5;
+constexpr int OFF_ABORT = OFF_BAR + 8 * NUM_BARS + 8;   // after the tensor-memory slot
+constexpr int SMEM_BYTES = OFF_ABORT + 8;
+constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
+static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
+
+struct Tile {
+  int m, tok0, ntok;
+};
+
+// Unit u of the order described above: units before units_full are whole tiles.
+__device__ __forceinline__ Tile tile_of(const Int8PairArgs &p, int u) {
+  int t = u, half = -1;
+  if (u >= p.units_full) {
+    const int h = u - p.units_full;
+    t = p.units_full + (h >> 1);
+    half = h & 1;
+  }
+  const int per = kGroupM * p.n_tiles;
+  const int g = t / per, i = t - g * per;
+  const int gm = min(kGroupM, p.m_tiles - g * kGroupM);
+  Tile r;
+  r.m = g * kGroupM + i % gm;
+  r.tok0 = (i / gm) * PN + (half > 0 ? HN : 0);
+  r.ntok = half < 0 ? PN : HN;
+  return r;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_gemm_2sm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                         const __grid_constant__ CUtensorMap tm_xh, const __grid_constant__ CUtensorMap tm_y,
+                         const Int8PairArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  auto sm_a = [&](int s) { return base + static_cast<uint32_t>(s) * STAGE_BYTES; };
+  auto sm_b = [&](int s) { return base + static_cast<uint32_t>(s) * STAGE_BYTES + A_BYTES; };
+  auto full = [&](int s) { return base + OFF_BAR + 8u * s; };
+  auto empty = [&](int s) { return base + OFF_BAR + 8u * (STAGES + s); };
+  auto acc_full = [&](int b) { return base + OFF_BAR + 8u * (2 * STAGES + b); };
+  auto acc_empty = [&](int b) { return base + OFF_BAR + 8u * (2 * STAGES + 2 + b); };
+  const uint32_t drain = base + OFF_BAR + 8u * (2 * STAGES + 4);
+  const uint32_t tmem_slot = base + OFF_BAR + 8u * NUM_BARS;
+  // (not a static variable: it would be padded to the alignment of the ring)
+  volatile int &s_abort = *reinterpret_cast<volatile int *>(smem_raw + (base - smem_u32(smem_raw)) + OFF_ABORT);
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster_id = blockIdx.x >> 1;
+  const int num_clusters = gridDim.x >> 1;
+  auto lead = [&](uint32_t local_addr) { return mapa_shared(local_addr, 0); };
+
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 8);   // 2 x 4 epilogue warps
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 4 && lane == 0) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_xh);
+  }
+  if (warp == 0 && lane == 0) tma_prefetch_desc(&tm_y);
+  if (warp == 5) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive_wait();   // the leader's barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = ld_shared_u32(tmem_slot);
+
+  if (warp == 5) {
+    // ---------------- MMA issue (even CTA) ----------------
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc_full = idesc_i8_s32(2 * PM, PN), idesc_half = idesc_i8_s32(2 * PM, HN);
+      const uint64_t a0 = smem_desc_sw128(sm_a(0), 16, 1024), b0 = smem_desc_sw128(sm_b(0), 16, 1024);
+      const uint32_t a_lo0 = static_cast<uint32_t>(a0), b_lo0 = static_cast<uint32_t>(b0);
+      const uint32_t hi = static_cast<uint32_t>(a0 >> 32);   // the same for both operands
+      int s = 0, tc = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = cluster_id; u < p.units && ok; u += num_clusters, ++tc) {
+        const uint32_t idesc = tile_of(p, u).ntok == PN ? idesc_full : idesc_half;
+        const uint32_t d = tmem + static_cast<uint32_t>((tc & 1) * PN);
+        if (!mbar_wait(acc_empty(tc & 1), ((tc >> 1) & 1) ^ 1, p.status)) { ok = false; break; }
+        tc_fence_after();
+        for (int ks = 0; ks < p.ksteps; ++ks) {
+          if (!mbar_wait(full(s), ph, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t off = static_cast<uint32_t>(s) * (STAGE_BYTES >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_ss_pair_i8_lo(d, a_lo0 + off + 2 * kk, hi, b_lo0 + off + 2 * kk, hi, idesc,
+                                 (ks > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_pair_mc(empty(s), 0x3);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(acc_full(tc & 1), 0x3);
+      }
+      if (!ok) s_abort = 1;
+      tc_commit_pair_mc(drain, 0x1);   // every MMA issued so far has completed
+      mbar_wait(drain, 0, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 4) {
+    // ---------------- TMA producer: this CTA's weight rows and token half ----------------
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true, dep_done = false;
+      for (int u = cluster_id; u < p.units && ok; u += num_clusters) {
+        const Tile w = tile_of(p, u);
+        const bool half = w.ntok != PN;
+        const int m0 = w.m * 2 * PM + static_cast<int>(rank) * PM;
+        const int t0 = w.tok0 + static_cast<int>(rank) * (w.ntok / 2);
+        const CUtensorMap *mx = half ? &tm_xh : &tm_x;
+        const uint32_t bytes = 2u * static_cast<uint32_t>(A_BYTES + (half ? B_BYTES / 2 : B_BYTES));
+        int ks = 0;
+        if (!dep_done) {
+          // the ring's first round: the weights load while the kernel before
+          // still quantizes the activations
+          const int n = min(STAGES, p.ksteps);
+          if (!p.early) grid_dep_wait();
+          for (int i = 0; i < n; ++i) {
+            if (leader) mbar_arrive_expect_tx(full(i), bytes);
+            tma_load_2d_pair(sm_a(i), &tm_w, lead(full(i)), i * KB, m0);
+          }
+          if (p.early) grid_dep_wait();
+          grid_dep_launch();
+          dep_done = true;
+          for (int i = 0; i < n; ++i) tma_load_2d_pair(sm_b(i), mx, lead(full(i)), i * KB, t0);
+          ks = n;
+          s = n == STAGES ? 0 : n;
+          ph = n == STAGES ? 1u : 0u;
+        }
+        for (; ks < p.ksteps; ++ks) {
+          if (s_abort || !mbar_wait(empty(s), ph ^ 1, p.status)) { ok = false; break; }
+          const uint32_t fb = lead(full(s));
+          if (leader) mbar_arrive_expect_tx(full(s), bytes);
+          tma_load_2d_pair(sm_a(s), &tm_w, fb, ks * KB, m0);
+          tma_load_2d_pair(sm_b(s), mx, fb, ks * KB, t0);
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!dep_done) {
+        grid_dep_wait();
+        grid_dep_launch();
+      }
+      if (!ok) {
+        s_abort = 1;
+        // loads still in flight land in this CTA's shared memory; give them time
+        // to finish (their completion is counted in the leader's barrier)
+        const uint64_t t_end = globaltimer() + 2000000ull;
+        while (globaltimer() < t_end) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue (warps 0-3) ----------------
+    // Lane l of warp q holds feature m = 32 q + l; features 0-63 go to box 0 of
+    // the staging chunk, 64-127 to box 1, each [64 tokens][64 features] with the
+    // 128-byte swizzle.  Lanes 2i and 2i + 1 swap one value so that each writes a
+    // BF16 pair of adjacent features: the even lane for token j, the odd lane for
+    // token j + 4 (j & 4 == 0), whose rows fall in complementary bank halves.
+    grid_dep_wait();   // sx may be the preceding kernel's output
+    const int q = warp;
+    const bool odd = (lane & 1) != 0;
+    const int fm = 32 * (q & 1) + static_cast<int>(lane & ~1u);
+    const uint32_t chunk = static_cast<uint32_t>(fm >> 3);
+    const uint32_t lane_base = base + OFF_OUT + static_cast<uint32_t>(q >> 1) * BOX_BYTES + (odd ? 4u * 128u : 0u) +
+                               static_cast<uint32_t>((fm & 7) >> 1) * 4u;
+    uint32_t xo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xo[i] = (chunk ^ static_cast<uint32_t>(i + (odd ? 4 : 0))) << 4;
+    int tc = 0, nchunk = 0;
+    bool ok = true;
+    for (int u = cluster_id; u < p.units && ok; u += num_clusters, ++tc) {
+      const Tile w = tile_of(p, u);
+      const int feat0 = w.m * 2 * PM + static_cast<int>(rank) * PM;
+      const int64_t n = static_cast<int64_t>(feat0) + threadIdx.x;
+      const float sw = n < p.N ? __ldcg(p.sw + n) : 0.f;
+      // the tile's token scales (the previous tile's were last read before its
+      // final staging barrier)
+      for (int i = static_cast<int>(threadIdx.x); i < w.ntok; i += 128) {
+        const float v = static_cast<int64_t>(w.tok0) + i < p.T ? __ldcg(p.sx + w.tok0 + i) : 0.f;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + OFF_SX + 4u * i), "f"(v) : "memory");
+      }
+      const bool fail = s_abort || !mbar_wait(acc_full(tc & 1), (tc >> 1) & 1, p.status);
+      if (named_bar_any(EPI_ANY_BAR, 128, fail)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>((tc & 1) * PN);
+      const int nch = w.ntok / CHUNK_T;
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c, ++nchunk) {
+        uint32_t ra[32], rb[32];
+        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * CHUNK_T), ra);
+        tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * CHUNK_T + 32), rb);
+        // the store that last used this staging chunk has finished reading it
+        if (threadIdx.x == 0) tma_store_wait_read<1>();
+        tc_wait_ld();
+        reg_fence(ra);
+        reg_fence(rb);
+        if (c == nch - 1) {
+          // every accumulator column is in registers: release it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead(acc_empty(tc & 1)));
+        }
+        named_bar_sync(EPI_BAR, 128);
+        const uint32_t out = lane_base + static_cast<uint32_t>(nchunk & 1) * CHUNK_BYTES;
+        const uint32_t sxa = base + OFF_SX + 4u * static_cast<uint32_t>(c * CHUNK_T);
+        auto emit = [&](const uint32_t (&r)[32], int j0) {
+#pragma unroll
+          for (int jj = 0; jj < 32; jj += 8) {
+            float sx[8];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(sx[0]), "=f"(sx[1]), "=f"(sx[2]), "=f"(sx[3])
+                         : "r"(sxa + 4u * (j0 + jj)));
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(sx[4]), "=f"(sx[5]), "=f"(sx[6]), "=f"(sx[7])
+                         : "r"(sxa + 4u * (j0 + jj + 4)));
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int32_t>(r[jj + i])), sx[i]), sw);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float recv = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 4], 1);
+              const uint32_t w2 = odd ? pack_bf16x2(recv, v[i + 4]) : pack_bf16x2(v[i], recv);
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(out + static_cast<uint32_t>(j0 + jj + i) * 128u + xo[i]),
+                           "r"(w2)
+                           : "memory");
+            }
+          }
+        };
+        emit(ra, 0);
+        emit(rb, 32);
+        fence_proxy_async_smem();
+        named_bar_sync(EPI_BAR, 128);
+        if (threadIdx.x == 0) {
+          for (int b = 0; b < 2; ++b)
+            tma_store_2d(&tm_y, base + OFF_OUT + static_cast<uint32_t>(nchunk & 1) * CHUNK_BYTES + b * BOX_BYTES,
+                         feat0 + 64 * b, w.tok0 + c * CHUNK_T);
+          tma_store_commit();
+        }
+      }
+    }
+    if (threadIdx.x == 0) tma_store_wait_all<0>();
+    if (!ok) s_abort = 1;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive_wait();   // both CTAs are done with the pair's tensor memory
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+cudaError_t launch_int8_gemm_2sm(const Int8PairArgs &args, const CUtensorMap &tm_w, const CUtensorMap &tm_x,
+                                 const CUtensorMap &tm_xh, const CUtensorMap &tm_y, int num_sms, cudaStream_t st,
+                                 bool pdl) {
+  Int8PairArgs p = args;
+  if (p.T <= 0 || p.N <= 0 || p.K <= 0 || p.N % 8 != 0) return cudaErrorInvalidValue;
+  p.m_tiles = static_cast<int>((p.N + 2 * PM - 1) / (2 * PM));
+  p.n_tiles = static_cast<int>((p.T + PN - 1) / PN);
+  p.ksteps = static_cast<int>((p.K + KB - 1) / KB);
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  if (2 * tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  const int64_t pairs = num_sms / 2;
+  // a last round at most half full runs its tiles as 128-token halves
+  const int64_t rem = tiles % pairs;
+  const bool halves = rem > 0 && 2 * rem <= pairs;
+  p.units_full = static_cast<int>(halves ? tiles - rem : tiles);
+  p.units = static_cast<int>(halves ? tiles + rem : tiles);
+  const int64_t clusters = p.units < pairs ? p.units : pairs;
+  cudaError_t e = ensure_smem_optin(reinterpret_cast<const void *>(int8_gemm_2sm_kernel), SMEM_ALLOC);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_ALLOC;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, int8_gemm_2sm_kernel, tm_w, tm_x, tm_xh, tm_y, p);
+}
+
+}  // namespace qlora

@@ -62,6 +62,7 @@ cudaError_t launch_dequantize_int8(const int8_t *codes, const float *scales, int
 // Y[T, N] = sx[t] sw[n] sum_k Xq[t, k] Wq[n, k] on kind::i8 (int8_gemm.cu)
 // ---------------------------------------------------------------------------
 struct Int8GemmGeom {
+  bool pair;            // 256 x 256 tiles on CTA pairs (the fields below do not apply)
   int nt;               // tokens per tile (the MMA's N): 16, 32, 64, 128 or 256
   int stages;           // TMA pipeline depth
   int smem;             // dynamic shared memory bytes
@@ -80,6 +81,21 @@ struct Int8GemmArgs {
 // maps: Wq [N rows, K bytes] box 128 x 128, Xq [T rows, K bytes] box nt x 128, 128-byte swizzle
 cudaError_t launch_int8_gemm(const Int8GemmArgs &a, const Int8GemmGeom &g, const CUtensorMap &tm_w,
                              const CUtensorMap &tm_x, cudaStream_t st, bool pdl);
+
+// The same product on CTA pairs, 256 x 256 tiles (int8_gemm_2sm.cu)
+struct Int8PairArgs {
+  int64_t T, N, K;
+  const float *sx, *sw;   // [T], [N]
+  uint32_t *status;
+  int early;              // as in Int8GemmArgs
+  int m_tiles, n_tiles, ksteps, units, units_full;   // (filled by the launcher)
+};
+// maps: Wq [N rows, K bytes] box 128 x 128; Xq [T rows, K bytes] box 128 x 128
+// and (xh, half tiles) 64 x 128; Y [T rows, N cols] BF16 box 64 x 64; all with
+// the 128-byte swizzle
+cudaError_t launch_int8_gemm_2sm(const Int8PairArgs &a, const CUtensorMap &tm_w, const CUtensorMap &tm_x,
+                                 const CUtensorMap &tm_xh, const CUtensorMap &tm_y, int num_sms, cudaStream_t st,
+                                 bool pdl);
 
 // ---------------------------------------------------------------------------
 // dA = dU^T Xq from the 8-bit activation (da_int8.cu)
