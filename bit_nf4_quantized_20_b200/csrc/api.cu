@@ -1370,7 +1370,7 @@ struct Int8Launch {
 static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, const qlora_int8_matrix *w, void *y,
                                  void *status, bool early, Int8Launch &l) {
   const int64_t N = w->rows, K = w->cols;
-  l.g = int8_gemm_geom(T, N, K);
+  l.g = int8_gemm_geom(T, N, K, num_sms_current());
   memset(&l.a, 0, sizeof(l.a));
   memset(&l.p, 0, sizeof(l.p));
   l.a.T = T;

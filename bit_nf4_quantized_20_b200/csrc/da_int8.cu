@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       int issued = 0;
       for (int st = 0; st < nst; ++st) {
         const int s = st % NR;
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = idesc_bf16_f32(AM, NB, true, false);
       bool ok = true;
       for (int st = 0; st < nst; ++st) {
@@ -307,13 +307,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = split * kThreads + static_cast<int>(threadIdx.x); i < items; i += splits * kThreads) {
     const int j = i >> 5, f = (i & 31) * 4;
     const uint32_t local = base + static_cast<uint32_t>(j * kPitch + f) * 4u;
+    float4 part[kMaxSplits];   // the cluster's loads all in flight
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)
+      if (k < splits) part[k] = ld_dsmem_f4(mapa_shared(local, static_cast<uint32_t>(k)));
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < splits; ++k) {   // split order: the sum does not depend on timing
-      const float4 p = ld_dsmem_f4(mapa_shared(local, static_cast<uint32_t>(k)));
-      s.x += p.x;
-      s.y += p.y;
-      s.z += p.z;
-      s.w += p.w;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k) {   // split order: the sum does not depend on timing
+      if (k < splits) {
+        s.x += part[k].x;
+        s.y += part[k].y;
+        s.z += part[k].z;
+        s.w += part[k].w;
+      }
     }
     if (k0 + f < a.K)   // K % 64 == 0
       *reinterpret_cast<uint2 *>(a.dA + static_cast<int64_t>(j) * a.K + k0 + f) =

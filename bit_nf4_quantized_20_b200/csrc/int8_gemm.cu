@@ -5,7 +5,7 @@
 //   Y[t, n]   = BF16_RNE(RN32(RN32(float(acc) * sx[t]) * sw[n]))
 //
 // One CTA owns 128 weight rows (the MMA's M) against nt tokens (its N, 16 to
-// 256: tokens past T arrive as zeros) over a range of the contraction; the
+// 128: tokens past T arrive as zeros) over a range of the contraction; the
 // weights stream through TMA once per token tile.  The ranges of a tile are
 // the CTAs of one cluster: each leaves its INT32 tile in its own shared memory
 // (the drained ring), token by token, and after a cluster barrier every CTA
@@ -19,11 +19,13 @@
 
 #include "common.cuh"
 #include "gemm_common.cuh"
+#include "int8_common.cuh"
 #include "kernels.h"
 
 namespace qlora {
 
 using namespace gemm;
+using int8::kPitch;
 
 namespace {
 
@@ -34,18 +36,8 @@ constexpr int kMaxStages = 8;
 constexpr int kThreads = 192;
 constexpr int kBarBytes = 8 * (2 * kMaxStages + 1) + 8;
 constexpr int kFixed = kBarBytes + 1024;      // + alignment slack for the swizzle atoms
-constexpr int kPitch = WM + 4;                // INT32 per token row of the partial tile
-constexpr int kMaxSmem = 220 * 1024;
+constexpr int kMaxSmem = 220 * 1024;   // three of the narrow tiles' 74 KiB rings share an SM
 constexpr int kMaxSplits = 8;
-
-__device__ __forceinline__ int4 ld_dsmem_i4(uint32_t cluster_addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(cluster_addr)
-               : "memory");
-  return v;
-}
 
 }  // namespace
 
@@ -102,7 +94,7 @@ __global__ void __launch_bounds__(kThreads)
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       if (!a.early) grid_dep_wait();
       const int lead = min(NS, nst);
       for (int st = 0; st < lead; ++st) {   // the ring's first round: nothing to wait for
@@ -113,10 +105,10 @@ __global__ void __launch_bounds__(kThreads)
       grid_dep_launch();
       for (int st = 0; st < lead; ++st)
         tma_load_2d(stage_x(st), &tm_x, full(st), (kb0 + st) * KB, static_cast<int32_t>(t0));
-      int issued = lead;
+      int issued = lead, s = lead == NS ? 0 : lead;
+      uint32_t ph = lead == NS ? 0u : 1u;   // parity of the slot's last release
       for (int st = lead; st < nst; ++st) {
-        const int s = st % NS;
-        if (s_abort || !mbar_wait(empty(s), ((st / NS) & 1) ^ 1, a.status)) {
+        if (s_abort || !mbar_wait_spin(empty(s), ph, a.status)) {
           s_abort = 1;
           break;
         }
@@ -124,6 +116,10 @@ __global__ void __launch_bounds__(kThreads)
         tma_load_2d(stage_w(s), &tm_w, full(s), (kb0 + st) * KB, static_cast<int32_t>(n0));
         tma_load_2d(stage_x(s), &tm_x, full(s), (kb0 + st) * KB, static_cast<int32_t>(t0));
         issued = st + 1;
+        if (++s == NS) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
       if (s_abort) {
         // every copy in flight lands before the CTA can exit
@@ -133,21 +129,38 @@ __global__ void __launch_bounds__(kThreads)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = idesc_i8_s32(WM, NT);
+      // one thread issues everything: the ring position, its barriers and the
+      // descriptors' low words advance by additions
+      const uint64_t w0 = smem_desc_sw128(stage_w(0), 16, 1024), x0 = smem_desc_sw128(stage_x(0), 16, 1024);
+      const uint32_t hi = static_cast<uint32_t>(w0 >> 32);   // the same for both operands
+      const uint32_t w_lo0 = static_cast<uint32_t>(w0), x_lo0 = static_cast<uint32_t>(x0);
+      uint32_t off = 0, ph = 0, fb = full(0), eb = empty(0), acc = 0;
+      int s = 0;
       bool ok = true;
       for (int st = 0; st < nst; ++st) {
-        const int s = st % NS;
-        if (!mbar_wait(full(s), (st / NS) & 1, a.status)) {
+        if (!mbar_wait_spin(fb, ph, a.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_ss_i8(tmem, smem_desc_sw128(stage_w(s) + kk * 32, 16, 1024),
-                       smem_desc_sw128(stage_x(s) + kk * 32, 16, 1024), idesc, (st > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(empty(s));
+        for (int kk = 0; kk < 4; ++kk) {
+          tc_mma_ss_i8_lo(tmem, w_lo0 + off + 2 * kk, hi, x_lo0 + off + 2 * kk, hi, idesc, acc);
+          acc = 1;
+        }
+        tc_commit(eb);
+        off += STAGE >> 4;
+        fb += 8;
+        eb += 8;
+        if (++s == NS) {
+          s = 0;
+          ph ^= 1u;
+          off = 0;
+          fb = full(0);
+          eb = empty(0);
+        }
       }
       if (!ok) s_abort = 1;
       tc_commit(acc_bar);   // also drains: arrives once everything issued has completed
@@ -166,54 +179,15 @@ __global__ void __launch_bounds__(kThreads)
     const bool have = __all_sync(0xffffffffu, !fail);   // tcgen05.ld is warp-collective
     tc_fence_after();
     const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-    for (int c0 = 0; c0 < tv; c0 += CW) {
-      uint32_t v[CW];
-      if (have) {
-        if constexpr (CW == 16) tmem_ld_32x32b_x16(trow + c0, v);
-        else tmem_ld_32x32b_x32(trow + c0, v);
-        tc_wait_ld();
-      } else {
-#pragma unroll
-        for (int j = 0; j < CW; ++j) v[j] = 0u;
-      }
-#pragma unroll
-      for (int j = 0; j < CW; ++j)
-        if (c0 + j < tv)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + static_cast<uint32_t>((c0 + j) * kPitch + row) * 4u),
-                       "r"(v[j])
-                       : "memory");
-    }
+    int8::tile_to_smem<CW>(trow, base, row, tv, have);
   }
   tc_fence_before();
   __syncwarp();
   if (splits > 1) cluster_arrive_wait();
   else __syncthreads();
 
-  // this CTA's share of the tile: groups of four features of a token, dealt to
-  // the cluster's threads in turn
-  const int items = tv * (WM / 4);
-  for (int i = split * kThreads + static_cast<int>(threadIdx.x); i < items; i += splits * kThreads) {
-    const int t = i >> 5, f = (i & 31) * 4;
-    const uint32_t local = base + static_cast<uint32_t>(t * kPitch + f) * 4u;
-    int4 s = make_int4(0, 0, 0, 0);
-    for (int k = 0; k < splits; ++k) {
-      const int4 p = ld_dsmem_i4(mapa_shared(local, static_cast<uint32_t>(k)));
-      s.x += p.x;
-      s.y += p.y;
-      s.z += p.z;
-      s.w += p.w;
-    }
-    if (n0 + f < a.N) {   // N % 8 == 0: four features are inside or outside together
-      const float sx = __ldcg(a.sx + t0 + t);
-      const float4 sw = __ldcg(reinterpret_cast<const float4 *>(a.sw + n0 + f));
-      const uint32_t y0 = pack_bf16x2(__fmul_rn(__fmul_rn(static_cast<float>(s.x), sx), sw.x),
-                                      __fmul_rn(__fmul_rn(static_cast<float>(s.y), sx), sw.y));
-      const uint32_t y1 = pack_bf16x2(__fmul_rn(__fmul_rn(static_cast<float>(s.z), sx), sw.z),
-                                      __fmul_rn(__fmul_rn(static_cast<float>(s.w), sx), sw.w));
-      *reinterpret_cast<uint2 *>(a.y + (t0 + t) * a.N + n0 + f) = make_uint2(y0, y1);
-    }
-  }
+  // this CTA's share of the tile
+  int8::join_splits(base, splits, split, 1u, 0u, tv, t0, n0, a.N, a.sx, a.sw, a.y);
   __syncwarp();
   // no CTA leaves (and frees its shared memory) while another still reads it
   if (splits > 1) cluster_arrive_wait();
@@ -224,23 +198,70 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-Int8GemmGeom int8_gemm_geom(int64_t T, int64_t N, int64_t K) {
+// The variant and its geometry.  Measured (microseconds, weights from HBM, 18
+// token counts on each of seven weight shapes):
+//   up to 32 tokens, one tile of 16 or 32: bound by the weights' bytes.  Split
+//   until every SM has a CTA (1 token on 1024 x 4096, 8 tiles: 3.4 with eight
+//   ranges, 3.7 with six), and on, up to three CTAs an SM, while a range keeps
+//   eight blocks (14336 x 4096, 112 tiles: 14.4 with two ranges, 13.5 with
+//   three; 4096 x 4096, 32 tiles: 6.9 with four, 7.9 with eight of four blocks;
+//   22016 x 1040, 172 tiles: 7.8 with one, 9.0 with two of five).
+//   More tokens: the least of these estimates, S = the contraction blocks of
+//   the SM with the most work:
+//     64-token tiles 4.2 + 0.27 S with one CTA an SM, 5.5 + 0.165 S with two,
+//     7.5 + 0.165 S with more; 128-token tiles 5.2 + 0.35 S and 7 + 0.27 S;
+//     pairs 4.2 + 0.185 S for half tiles, 6 + 0.31 S with full ones;
+//     none less than 4 + the weights' bytes at 6 TB/s.
+//   (256 tokens: 4096 x 4096 10.8 split against 10.9 on pairs, 4096 x 14336
+//   21.9 against 27.8, 14336 x 4096 25.8 against 17.9.)
+//   Ranges come in powers of two there: with one CTA an SM, clusters of three
+//   leave SMs of a GPU partition idle (1024 x 4096, 768 tokens, 48 tiles: 15.4
+//   with three ranges, 10.9 with two).
+Int8GemmGeom int8_gemm_geom(int64_t T, int64_t N, int64_t K, int num_sms) {
   Int8GemmGeom g;
-  g.pair = T > 256;
-  g.nt = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-  const int stage = W_BYTES + g.nt * KB;
-  g.stages = g.nt <= 32 ? 4 : g.nt <= 128 ? 3 : 4;
-  g.smem = g.stages * stage + kFixed;
-  const int per_sm = kMaxSmem / g.smem < 1 ? 1 : kMaxSmem / g.smem;
-  const int64_t tiles = (N + WM - 1) / WM * ((T + g.nt - 1) / g.nt);
-  const int64_t kb = (K + KB - 1) / KB;
-  // one wave of CTAs; at least two contraction blocks each
-  int64_t s = static_cast<int64_t>(per_sm) * 148 / tiles;
-  if (s > kMaxSplits) s = kMaxSplits;
-  if (s > (kb + 1) / 2) s = (kb + 1) / 2;
-  if (s < 1) s = 1;
-  g.kb_per_split = static_cast<int>((kb + s - 1) / s);
-  g.splits = static_cast<int>((kb + g.kb_per_split - 1) / g.kb_per_split);
+  const int64_t rows = (N + WM - 1) / WM, kb = (K + KB - 1) / KB;
+  auto set = [&](int nt, int stages, int64_t splits) {
+    g.nt = nt;
+    g.stages = stages;
+    g.smem = stages * (W_BYTES + nt * KB) + kFixed;
+    g.kb_per_split = static_cast<int>((kb + splits - 1) / splits);
+    g.splits = static_cast<int>((kb + g.kb_per_split - 1) / g.kb_per_split);
+  };
+  g.pair = false;
+  if (T <= 32) {
+    int64_t s = 1;
+    while (s < kMaxSplits && s < kb &&
+           (rows * (s + 1) <= num_sms || (kb / (s + 1) >= 8 && rows * (s + 1) <= 3 * static_cast<int64_t>(num_sms))))
+      ++s;
+    const int nt = T <= 16 ? 16 : 32;
+    // three 32-token rings of four stages do not share an SM
+    set(nt, nt == 32 && rows * s > 2 * static_cast<int64_t>(num_sms) ? 3 : 4, s);
+    return g;
+  }
+  double best = 0.0;
+  for (int nt = 64; nt <= 128; nt *= 2) {
+    if (nt / 2 >= T) break;
+    const int64_t tiles = rows * ((T + nt - 1) / nt);
+    for (int64_t s = 1; s <= kMaxSplits && s <= kb; s *= 2) {
+      const int64_t ctas = tiles * s, waves = (ctas + num_sms - 1) / num_sms, per = (kb + s - 1) / s;
+      if (s > 1 && waves > (nt == 64 ? 3 : 2)) break;
+      const double work = static_cast<double>(waves * per);
+      const double t = nt == 64 ? (waves == 1 ? 4.2 + 0.27 * work : (waves == 2 ? 5.5 : 7.5) + 0.165 * work)
+                                : (waves == 1 ? 5.2 + 0.35 * work : 7.0 + 0.27 * work);
+      if (best == 0.0 || t < best) {
+        best = t;
+        set(nt, waves == 1 || (nt == 64 && waves == 2) ? 4 : 3, s);
+      }
+    }
+  }
+  const double weights = 4.0 + static_cast<double>(N) * static_cast<double>(K) / 6e6;
+  const Int8PairUnits w = int8_pair_units(T, N, num_sms);
+  double pair = (w.rounds_full > 0 ? 6.0 : 4.2) +
+                static_cast<double>(kb) * (0.31 * w.rounds_full + 0.185 * w.rounds_half);
+  best = best > weights ? best : weights;
+  pair = pair > weights ? pair : weights;
+  // (the one-CTA grid holds 65535 token tiles)
+  g.pair = pair <= best || (T + g.nt - 1) / g.nt > 65535;
   return g;
 }
 
@@ -296,7 +317,6 @@ cudaError_t launch_int8_gemm(const Int8GemmArgs &a, const Int8GemmGeom &g, const
     case 32: return launch_nt<32>(a, g, tm_w, tm_x, st, pdl);
     case 64: return launch_nt<64>(a, g, tm_w, tm_x, st, pdl);
     case 128: return launch_nt<128>(a, g, tm_w, tm_x, st, pdl);
-    case 256: return launch_nt<256>(a, g, tm_w, tm_x, st, pdl);
     default: return cudaErrorInvalidValue;
   }
 }

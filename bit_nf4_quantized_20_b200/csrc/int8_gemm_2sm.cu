@@ -9,14 +9,13 @@
 // by TMA (32 KiB), so an operand byte feeds 256 products; six stages are in
 // flight.  Two 256-column INT32 accumulators in tensor memory let the epilogue
 // of one tile run under the next tile's MMAs: tcgen05.ld, conversion and the
-// two scales, BF16 pairs into a swizzled 64-token staging chunk (two of them in
-// turn), TMA store.
+// two scales, BF16 pairs into a swizzled 64-token staging chunk, TMA store; two
+// groups of four warps with a staging chunk each.
 //
 // Bound by the tensor cores; the tiles run in blocks of eight weight tiles by
 // all token tiles, so that the pairs running at one time share operands in L2.
-// A last round at most half full runs its tiles as 128-token halves.
 //
-// Warps: 0-3 epilogue, 4 TMA, 5 paired tensor-memory allocation and, on the
+// Warps: 0-7 epilogue, 8 TMA, 9 paired tensor-memory allocation and, on the
 // even CTA, the MMA issue.
 
 #include "common.cuh"
@@ -40,10 +39,10 @@ constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int CHUNK_T = 64;                    // tokens per staging chunk
 constexpr int BOX_BYTES = CHUNK_T * 128;       // 64 tokens x 64 features, BF16
 constexpr int CHUNK_BYTES = 2 * BOX_BYTES;
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kTmemCols = 512;
 constexpr int kGroupM = 8;                     // weight tiles per block of tiles
-constexpr int EPI_BAR = 1, EPI_ANY_BAR = 2;
+constexpr int kEpiWarps = 8;                   // two groups of four
 
 constexpr int OFF_OUT = STAGES * STAGE_BYTES;
 constexpr int OFF_SX = OFF_OUT + 2 * CHUNK_BYTES;
@@ -59,21 +58,27 @@ struct Tile {
   int m, tok0, ntok;
 };
 
-// Unit u of the order described above: units before units_full are whole tiles.
-__device__ __forceinline__ Tile tile_of(const Int8PairArgs &p, int u) {
-  int t = u, half = -1;
-  if (u >= p.units_full) {
-    const int h = u - p.units_full;
-    t = p.units_full + (h >> 1);
-    half = h & 1;
-  }
-  const int per = kGroupM * p.n_tiles;
-  const int g = t / per, i = t - g * per;
-  const int gm = min(kGroupM, p.m_tiles - g * kGroupM);
+// Full tiles run in blocks of kGroupM weight tiles by all token tiles.
+__device__ __forceinline__ Tile tile_of(const Int8PairUnits &w, int u) {
   Tile r;
+  r.ntok = u < w.full ? PN : HN;
+  int t = u, half = 0;
+  if (u >= w.full) {
+    const int h = u - w.full;
+    t = w.full + (h >> 1);
+    half = h & 1;
+    const int all = w.m_tiles * w.n_full;
+    if (t >= all) {   // the half tiles of the last token tile
+      r.m = h - 2 * (all - w.full);
+      r.tok0 = w.n_full * PN;
+      return r;
+    }
+  }
+  const int per = kGroupM * w.n_full;
+  const int g = t / per, i = t - g * per;
+  const int gm = min(kGroupM, w.m_tiles - g * kGroupM);
   r.m = g * kGroupM + i % gm;
-  r.tok0 = (i / gm) * PN + (half > 0 ? HN : 0);
-  r.ntok = half < 0 ? PN : HN;
+  r.tok0 = (i / gm) * PN + half * HN;
   return r;
 }
 
@@ -102,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool leader = rank == 0;
   const int cluster_id = blockIdx.x >> 1;
   const int num_clusters = gridDim.x >> 1;
+  const int n_units = p.units.full + p.units.halves;
   auto lead = [&](uint32_t local_addr) { return mapa_shared(local_addr, 0); };
 
   if (threadIdx.x == 0) {
@@ -112,18 +118,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 8);   // 2 x 4 epilogue warps
+      mbar_init(acc_empty(b), 2 * kEpiWarps);   // both CTAs'
     }
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_xh);
   }
   if (warp == 0 && lane == 0) tma_prefetch_desc(&tm_y);
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
@@ -133,9 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ld_shared_u32(tmem_slot);
 
-  if (warp == 5) {
+  if (warp == 9) {
     // ---------------- MMA issue (even CTA) ----------------
-    if (leader && lane == 0) {
+    if (leader && elect_one()) {
       constexpr uint32_t idesc_full = idesc_i8_s32(2 * PM, PN), idesc_half = idesc_i8_s32(2 * PM, HN);
       const uint64_t a0 = smem_desc_sw128(sm_a(0), 16, 1024), b0 = smem_desc_sw128(sm_b(0), 16, 1024);
       const uint32_t a_lo0 = static_cast<uint32_t>(a0), b_lo0 = static_cast<uint32_t>(b0);
@@ -143,13 +149,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, tc = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int u = cluster_id; u < p.units && ok; u += num_clusters, ++tc) {
-        const uint32_t idesc = tile_of(p, u).ntok == PN ? idesc_full : idesc_half;
+      for (int u = cluster_id; u < n_units && ok; u += num_clusters, ++tc) {
+        const uint32_t idesc = tile_of(p.units, u).ntok == PN ? idesc_full : idesc_half;
         const uint32_t d = tmem + static_cast<uint32_t>((tc & 1) * PN);
         if (!mbar_wait(acc_empty(tc & 1), ((tc >> 1) & 1) ^ 1, p.status)) { ok = false; break; }
         tc_fence_after();
         for (int ks = 0; ks < p.ksteps; ++ks) {
-          if (!mbar_wait(full(s), ph, p.status)) { ok = false; break; }
+          if (!mbar_wait_spin(full(s), ph, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t off = static_cast<uint32_t>(s) * (STAGE_BYTES >> 4);
 #pragma unroll
@@ -170,14 +176,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(drain, 0, p.status);
     }
     __syncwarp();
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ---------------- TMA producer: this CTA's weight rows and token half ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t ph = 0;
       bool ok = true, dep_done = false;
-      for (int u = cluster_id; u < p.units && ok; u += num_clusters) {
-        const Tile w = tile_of(p, u);
+      for (int u = cluster_id; u < n_units && ok; u += num_clusters) {
+        const Tile w = tile_of(p.units, u);
         const bool half = w.ntok != PN;
         const int m0 = w.m * 2 * PM + static_cast<int>(rank) * PM;
         const int t0 = w.tok0 + static_cast<int>(rank) * (w.ntok / 2);
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph = n == STAGES ? 1u : 0u;
         }
         for (; ks < p.ksteps; ++ks) {
-          if (s_abort || !mbar_wait(empty(s), ph ^ 1, p.status)) { ok = false; break; }
+          if (s_abort || !mbar_wait_spin(empty(s), ph ^ 1, p.status)) { ok = false; break; }
           const uint32_t fb = lead(full(s));
           if (leader) mbar_arrive_expect_tx(full(s), bytes);
           tma_load_2d_pair(sm_a(s), &tm_w, fb, ks * KB, m0);
@@ -228,58 +234,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ---------------- epilogue (warps 0-3) ----------------
-    // Lane l of warp q holds feature m = 32 q + l; features 0-63 go to box 0 of
-    // the staging chunk, 64-127 to box 1, each [64 tokens][64 features] with the
-    // 128-byte swizzle.  Lanes 2i and 2i + 1 swap one value so that each writes a
-    // BF16 pair of adjacent features: the even lane for token j, the odd lane for
+    // ---------------- epilogue (warps 0-7) ----------------
+    // Two groups of four warps; group e takes the 64-token chunks c with c % 2
+    // == e, each through its own staging chunk.  Lane l of warp q (of a group)
+    // holds feature m = 32 q + l; features 0-63 go to box 0 of the staging
+    // chunk, 64-127 to box 1, each [64 tokens][64 features] with the 128-byte
+    // swizzle.  Lanes 2i and 2i + 1 swap one value so that each writes a BF16
+    // pair of adjacent features: the even lane for token j, the odd lane for
     // token j + 4 (j & 4 == 0), whose rows fall in complementary bank halves.
     grid_dep_wait();   // sx may be the preceding kernel's output
-    const int q = warp;
+    const int q = warp & 3, grp = warp >> 2;
+    const int et = static_cast<int>(threadIdx.x) & 127;   // thread of the group
+    const int bar = 1 + grp;
     const bool odd = (lane & 1) != 0;
     const int fm = 32 * (q & 1) + static_cast<int>(lane & ~1u);
     const uint32_t chunk = static_cast<uint32_t>(fm >> 3);
-    const uint32_t lane_base = base + OFF_OUT + static_cast<uint32_t>(q >> 1) * BOX_BYTES + (odd ? 4u * 128u : 0u) +
-                               static_cast<uint32_t>((fm & 7) >> 1) * 4u;
+    const uint32_t stage = base + OFF_OUT + static_cast<uint32_t>(grp) * CHUNK_BYTES;
+    const uint32_t out = stage + static_cast<uint32_t>(q >> 1) * BOX_BYTES + (odd ? 4u * 128u : 0u) +
+                         static_cast<uint32_t>((fm & 7) >> 1) * 4u;
     uint32_t xo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) xo[i] = (chunk ^ static_cast<uint32_t>(i + (odd ? 4 : 0))) << 4;
-    int tc = 0, nchunk = 0;
+    int tc = 0;
     bool ok = true;
-    for (int u = cluster_id; u < p.units && ok; u += num_clusters, ++tc) {
-      const Tile w = tile_of(p, u);
+    for (int u = cluster_id; u < n_units && ok; u += num_clusters, ++tc) {
+      const Tile w = tile_of(p.units, u);
       const int feat0 = w.m * 2 * PM + static_cast<int>(rank) * PM;
-      const int64_t n = static_cast<int64_t>(feat0) + threadIdx.x;
+      const int64_t n = static_cast<int64_t>(feat0) + et;
       const float sw = n < p.N ? __ldcg(p.sw + n) : 0.f;
-      // the tile's token scales (the previous tile's were last read before its
-      // final staging barrier)
-      for (int i = static_cast<int>(threadIdx.x); i < w.ntok; i += 128) {
-        const float v = static_cast<int64_t>(w.tok0) + i < p.T ? __ldcg(p.sx + w.tok0 + i) : 0.f;
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + OFF_SX + 4u * i), "f"(v) : "memory");
-      }
+      // the scales of this group's chunks (those of the tile before were last
+      // read before its last barrier)
+      const int tok = (2 * (et >> 6) + grp) * CHUNK_T + (et & 63);
+      const float sxv = tok < w.ntok && static_cast<int64_t>(w.tok0) + tok < p.T ? __ldcg(p.sx + w.tok0 + tok) : 0.f;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + OFF_SX + 4u * tok), "f"(sxv) : "memory");
       const bool fail = s_abort || !mbar_wait(acc_full(tc & 1), (tc >> 1) & 1, p.status);
-      if (named_bar_any(EPI_ANY_BAR, 128, fail)) { ok = false; break; }
+      if (named_bar_any(bar, 128, fail)) { ok = false; break; }
       tc_fence_after();
       const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>((tc & 1) * PN);
       const int nch = w.ntok / CHUNK_T;
 #pragma unroll 1
-      for (int c = 0; c < nch; ++c, ++nchunk) {
+      for (int c = grp; c < nch; c += 2) {
         uint32_t ra[32], rb[32];
         tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * CHUNK_T), ra);
         tmem_ld_32x32b_x32(t_row + static_cast<uint32_t>(c * CHUNK_T + 32), rb);
-        // the store that last used this staging chunk has finished reading it
-        if (threadIdx.x == 0) tma_store_wait_read<1>();
+        // the store of this group's chunk before has finished reading it
+        if (et == 0) tma_store_wait_read<0>();
         tc_wait_ld();
         reg_fence(ra);
         reg_fence(rb);
-        if (c == nch - 1) {
-          // every accumulator column is in registers: release it
+        if (c + 2 >= nch) {
+          // this warp's accumulator columns are all in registers: release them
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(lead(acc_empty(tc & 1)));
         }
-        named_bar_sync(EPI_BAR, 128);
-        const uint32_t out = lane_base + static_cast<uint32_t>(nchunk & 1) * CHUNK_BYTES;
+        named_bar_sync(bar, 128);
         const uint32_t sxa = base + OFF_SX + 4u * static_cast<uint32_t>(c * CHUNK_T);
         auto emit = [&](const uint32_t (&r)[32], int j0) {
 #pragma unroll
@@ -308,26 +317,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         emit(ra, 0);
         emit(rb, 32);
         fence_proxy_async_smem();
-        named_bar_sync(EPI_BAR, 128);
-        if (threadIdx.x == 0) {
+        named_bar_sync(bar, 128);
+        if (et == 0) {
           for (int b = 0; b < 2; ++b)
-            tma_store_2d(&tm_y, base + OFF_OUT + static_cast<uint32_t>(nchunk & 1) * CHUNK_BYTES + b * BOX_BYTES,
-                         feat0 + 64 * b, w.tok0 + c * CHUNK_T);
+            tma_store_2d(&tm_y, stage + b * BOX_BYTES, feat0 + 64 * b, w.tok0 + c * CHUNK_T);
           tma_store_commit();
         }
       }
     }
-    if (threadIdx.x == 0) tma_store_wait_all<0>();
+    if (et == 0) tma_store_wait_all<0>();
     if (!ok) s_abort = 1;
   }
 
   tc_fence_before();
   __syncthreads();
   cluster_arrive_wait();   // both CTAs are done with the pair's tensor memory
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
+}
+
+// A half tile takes 0.6 of a full one's time (its weight rows load all the
+// same).  The tiles of a last round that is not full run as halves when that
+// ends sooner; a last token tile of at most 128 tokens is one half.
+Int8PairUnits int8_pair_units(int64_t T, int64_t N, int num_sms) {
+  const int pairs = num_sms / 2;
+  const int64_t cols = (T + HN - 1) / HN;
+  Int8PairUnits best;
+  double best_t = 0.0;
+  for (int split = 0; split < 2; ++split) {
+    Int8PairUnits w;
+    w.m_tiles = static_cast<int>((N + 2 * PM - 1) / (2 * PM));
+    w.n_full = static_cast<int>(cols / 2);
+    const int64_t tiles = static_cast<int64_t>(w.m_tiles) * w.n_full;
+    const int64_t last = split ? tiles % pairs : 0;
+    w.full = static_cast<int>(tiles - last);
+    w.halves = static_cast<int>(2 * last + (cols % 2) * w.m_tiles);
+    // unit u runs on pair u % pairs: the pairs before `full % pairs` have one
+    // full tile more than the others, who take the first halves
+    const int base = w.full / pairs, extra = w.full % pairs, total = w.full + w.halves;
+    double t = 0.0;
+    for (int c = 0; c < 2; ++c) {   // a pair with the extra full tile, and one without
+      const int pair = c == 0 ? (extra > 0 ? 0 : -1) : (extra < pairs ? extra : -1);
+      if (pair < 0 || pair >= total) continue;
+      const int f = base + (pair < extra ? 1 : 0), h = (total - pair + pairs - 1) / pairs - f;
+      if (f + 0.6 * h > t) {
+        t = f + 0.6 * h;
+        w.rounds_full = f;
+        w.rounds_half = h;
+      }
+    }
+    if (split == 0 || t < best_t) {
+      best = w;
+      best_t = t;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_int8_gemm_2sm(const Int8PairArgs &args, const CUtensorMap &tm_w, const CUtensorMap &tm_x,
@@ -335,18 +381,11 @@ cudaError_t launch_int8_gemm_2sm(const Int8PairArgs &args, const CUtensorMap &tm
                                  bool pdl) {
   Int8PairArgs p = args;
   if (p.T <= 0 || p.N <= 0 || p.K <= 0 || p.N % 8 != 0) return cudaErrorInvalidValue;
-  p.m_tiles = static_cast<int>((p.N + 2 * PM - 1) / (2 * PM));
-  p.n_tiles = static_cast<int>((p.T + PN - 1) / PN);
   p.ksteps = static_cast<int>((p.K + KB - 1) / KB);
-  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  if (2 * tiles > 0x7fffffff) return cudaErrorInvalidValue;
-  const int64_t pairs = num_sms / 2;
-  // a last round at most half full runs its tiles as 128-token halves
-  const int64_t rem = tiles % pairs;
-  const bool halves = rem > 0 && 2 * rem <= pairs;
-  p.units_full = static_cast<int>(halves ? tiles - rem : tiles);
-  p.units = static_cast<int>(halves ? tiles + rem : tiles);
-  const int64_t clusters = p.units < pairs ? p.units : pairs;
+  if ((p.N + 2 * PM - 1) / (2 * PM) * ((p.T + HN - 1) / HN) > 0x3fffffff) return cudaErrorInvalidValue;
+  p.units = int8_pair_units(p.T, p.N, num_sms);
+  const int64_t units = p.units.full + static_cast<int64_t>(p.units.halves), pairs = num_sms / 2;
+  const int64_t clusters = units < pairs ? units : pairs;
   cudaError_t e = ensure_smem_optin(reinterpret_cast<const void *>(int8_gemm_2sm_kernel), SMEM_ALLOC);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -63,13 +63,13 @@ cudaError_t launch_dequantize_int8(const int8_t *codes, const float *scales, int
 // ---------------------------------------------------------------------------
 struct Int8GemmGeom {
   bool pair;            // 256 x 256 tiles on CTA pairs (the fields below do not apply)
-  int nt;               // tokens per tile (the MMA's N): 16, 32, 64, 128 or 256
+  int nt;               // tokens per tile (the MMA's N): 16, 32, 64 or 128
   int stages;           // TMA pipeline depth
   int smem;             // dynamic shared memory bytes
   int splits;           // contraction splits of a tile: the CTAs of one cluster
   int kb_per_split;     // 128-byte contraction blocks per split
 };
-Int8GemmGeom int8_gemm_geom(int64_t T, int64_t N, int64_t K);
+Int8GemmGeom int8_gemm_geom(int64_t T, int64_t N, int64_t K, int num_sms);
 struct Int8GemmArgs {
   int64_t T, N, K;
   const float *sx, *sw;   // [T], [N]
@@ -82,13 +82,24 @@ struct Int8GemmArgs {
 cudaError_t launch_int8_gemm(const Int8GemmArgs &a, const Int8GemmGeom &g, const CUtensorMap &tm_w,
                              const CUtensorMap &tm_x, cudaStream_t st, bool pdl);
 
-// The same product on CTA pairs, 256 x 256 tiles (int8_gemm_2sm.cu)
+// The same product on CTA pairs, 256 x 256 tiles (int8_gemm_2sm.cu).  Work
+// units, dealt to the pairs in turn: full tiles first, then 128-token halves.
+struct Int8PairUnits {
+  int m_tiles;          // tiles of 256 weight rows
+  int n_full;           // token tiles of 256
+  int full;             // units 0 .. full - 1: tiles 0 .. full - 1
+  int halves;           // units after them: the remaining full tiles as two halves each, then
+                        // the half tiles of a last token tile of at most 128 tokens
+  int rounds_full, rounds_half;   // units of the pair with the longest run, full and half
+};
+Int8PairUnits int8_pair_units(int64_t T, int64_t N, int num_sms);
 struct Int8PairArgs {
   int64_t T, N, K;
   const float *sx, *sw;   // [T], [N]
   uint32_t *status;
   int early;              // as in Int8GemmArgs
-  int m_tiles, n_tiles, ksteps, units, units_full;   // (filled by the launcher)
+  int ksteps;             // (filled by the launcher)
+  Int8PairUnits units;    // (filled by the launcher)
 };
 // maps: Wq [N rows, K bytes] box 128 x 128; Xq [T rows, K bytes] box 128 x 128
 // and (xh, half tiles) 64 x 128; Y [T rows, N cols] BF16 box 64 x 64; all with
