@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       // the sU planes of the block's tokens, once
       mbar_arrive_expect_tx(su_full, static_cast<uint32_t>(tt_n) * 4u * su_box);
       for (int i = 0; i < tt_n; ++i)
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc_u = idesc_bf16_f32(DT, UB, false, true);
       const uint32_t idesc_b = idesc_bf16_f32(DN, static_cast<uint32_t>(2 * RB), true, false);
       bool ok = mbar_wait(su_full, 0, a.status);

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (warp == 17) {
     // ---------------- MMA issuer (even CTA) ----------------
-    if (leader && lane == 0) {
+    if (leader && elect_one()) {
       // The issuing thread shares its scheduler and ALU pipe with three
       // dequantization warps, so a stage costs it as few instructions as
       // possible: the ring position, the phase, the stage's barrier addresses
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else if (warp == 16) {
     // ---------------- TMA producer: this CTA's token half ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       int it = 0;
       bool ok = true, dep_done = false;
       for (int u = cluster_id; u < p.units && ok; u += num_clusters) {

@@ -182,7 +182,7 @@ __device__ __forceinline__ void skinny_tc_body(const CUtensorMap *tm_p, const CU
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       int issued = 0;
       for (int st = 0; st < nst; ++st) {
         const int s = st % NS;
@@ -218,7 +218,7 @@ __device__ __forceinline__ void skinny_tc_body(const CUtensorMap *tm_p, const CU
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = idesc_bf16_f32(TBM, static_cast<uint32_t>(NB), a.p_col != 0, a.q_cj != 0);
       bool ok = true;
       for (int st = 0; st < nst; ++st) {
