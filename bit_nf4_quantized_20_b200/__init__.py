@@ -429,23 +429,40 @@ class QuantizedInt8:
             raise ValueError(f"scales must be [{groups}, {rows}], got {list(scales.shape)}")
         if scales.device != codes.device:
             raise ValueError(f"scales is on {scales.device}, codes on {codes.device}")
+        self._set(codes, scales, rows, cols, group, codes.device)
+
+    def _set(self, codes, scales, rows, cols, group, device):
         self.codes, self.scales, self.rows, self.cols, self.group = codes, scales, rows, cols, group
-        self.device = codes.device
+        self.device = device
         self._struct = _lib.Int8Matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, group)
         self._ref = C.byref(self._struct)
-        _status(self.device)   # before any capture
+        _status(device)   # before any capture
+
+    @classmethod
+    def _of(cls, *args) -> "QuantizedInt8":
+        """Of buffers known to fit (no checks)."""
+        self = cls.__new__(cls)
+        self._set(*args)
+        return self
 
     def nbytes(self) -> int:
         return self.codes.numel() + 4 * self.scales.numel()
 
 
+# the current stream's handle by device index, without a Stream object (2 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _int8_call(device: torch.device, fn: str, *args) -> None:
-    """Call an entry point with `device` current (its launches go there)."""
-    if device.index == torch.cuda.current_device():
-        st = getattr(lib(), fn)(*args)
+    """Call an entry point on `device`'s current stream (its last argument)
+    with `device` current (its launches go there)."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = getattr(lib(), fn)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = getattr(lib(), fn)(*args)
+            st = getattr(lib(), fn)(*args, _raw_stream(index))
     if st:
         check(fn, st)
 
@@ -463,9 +480,10 @@ def quantize_int8(x: torch.Tensor, group: int = 0) -> QuantizedInt8:
         raise ValueError(f"group must be 0 (one scale a row) or {_INT8_GROUP}")
     rows, cols = x.shape
     dev = x.device
-    out = QuantizedInt8(torch.empty(rows, cols, dtype=torch.int8, device=dev),
-                        torch.empty(-(-cols // group) if group else 1, rows, dtype=torch.float32, device=dev), group)
-    _int8_call(dev, "qlora_quantize_int8", x.data_ptr(), rows, cols, group, out._ref, _stream(dev))
+    out = QuantizedInt8._of(torch.empty(rows, cols, dtype=torch.int8, device=dev),
+                            torch.empty(-(-cols // group) if group else 1, rows, dtype=torch.float32, device=dev),
+                            rows, cols, group, dev)
+    _int8_call(dev, "qlora_quantize_int8", x.data_ptr(), rows, cols, group, out._ref)
     return out
 
 
@@ -475,8 +493,7 @@ def quantize_int8_into(x: torch.Tensor, out: QuantizedInt8) -> QuantizedInt8:
     _need_cuda("x", x)
     if tuple(x.shape) != (out.rows, out.cols) or x.device != out.device:
         raise ValueError(f"x must be [{out.rows}, {out.cols}] on {out.device}")
-    _int8_call(out.device, "qlora_quantize_int8", x.data_ptr(), out.rows, out.cols, out.group, out._ref,
-               _stream(out.device))
+    _int8_call(out.device, "qlora_quantize_int8", x.data_ptr(), out.rows, out.cols, out.group, out._ref)
     return out
 
 
@@ -487,7 +504,7 @@ def dequantize_int8(q8: QuantizedInt8, out: torch.Tensor | None = None) -> torch
         out = torch.empty(q8.rows, q8.cols, dtype=torch.bfloat16, device=dev)
     else:
         _check_out("out", out, (q8.rows, q8.cols), dev)
-    _int8_call(dev, "qlora_dequantize_int8", q8._ref, out.data_ptr(), _stream(dev))
+    _int8_call(dev, "qlora_dequantize_int8", q8._ref, out.data_ptr())
     return out
 
 
@@ -517,7 +534,7 @@ def linear_int8(x, w8: QuantizedInt8, out: torch.Tensor | None = None) -> torch.
     else:
         _check_out("out", out, (T, w8.rows), dev)
     if given:
-        _int8_call(dev, "qlora_linear_int8_q", x._ref, w8._ref, out.data_ptr(), _status(dev), _stream(dev))
+        _int8_call(dev, "qlora_linear_int8_q", x._ref, w8._ref, out.data_ptr(), _status(dev))
     else:
         # the quantized tokens live for this call only (the allocator hands the
         # block to work that follows on this stream, or keeps it in the pool of
@@ -525,7 +542,7 @@ def linear_int8(x, w8: QuantizedInt8, out: torch.Tensor | None = None) -> torch.
         n = lib().qlora_linear_int8_scratch_bytes(T, K)
         scratch = torch.empty(n, dtype=torch.uint8, device=dev)
         _int8_call(dev, "qlora_linear_int8", x.data_ptr(), T, w8._ref, out.data_ptr(), scratch.data_ptr(), n,
-                   _status(dev), _stream(dev))
+                   _status(dev))
     return out
 
 
@@ -557,7 +574,7 @@ def linear_bwd_saved_int8(dy: torch.Tensor, x8: QuantizedInt8, qw: QuantizedNF4,
     st = qw.struct()
     _int8_call(dev, "qlora_linear_bwd_saved_int8", dy.data_ptr(), x8._ref, C.byref(st), A.data_ptr(), B.data_ptr(), r,
                float(s), u_saved.data_ptr(), dx.data_ptr(), dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), n,
-               _status(dev), _stream(dev))
+               _status(dev))
     return dx, dA, dB
 
 
