@@ -64,7 +64,7 @@ def check_quantize(x, group):
 @pytest.mark.parametrize("group", [0, 128])
 @pytest.mark.parametrize("rows,cols", [
     (1, 16), (1, 64), (3, 80), (7, 128), (9, 144), (17, 1024), (5, 1040), (33, 4096), (2, 4112), (4, 14336), (3, 16400),
-    (2, 22016), (2, 40000), (1000, 272),
+    (2, 22016), (2, 40000), (1000, 272), (1027, 1040), (1025, 2048),
 ])
 def test_quantize_dequantize_bitexact(rows, cols, group):
     check_quantize(activation(rows, cols, rows * 100003 + cols), group)
