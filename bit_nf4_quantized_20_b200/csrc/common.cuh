@@ -356,6 +356,12 @@ __device__ __forceinline__ void cluster_arrive_wait() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The same without ordering memory: for a barrier that only keeps every CTA
+// alive until the others have read its shared memory.
+__device__ __forceinline__ void cluster_arrive_wait_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // Shared::cluster address of the same shared-memory offset in CTA `rank`.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t local, uint32_t rank) {
   uint32_t r;

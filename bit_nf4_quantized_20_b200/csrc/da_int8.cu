@@ -10,21 +10,24 @@
 // codes, integers of at most 7 bits and a sign, are exact in BF16.  The product
 // then runs on tcgen05.mma kind::f16 with nothing of the activation rounded.
 // dU arrives as its hi and lo planes; (hi + lo) scale is split again into a hi
-// and a lo plane (about 16 significant bits), two MMAs into one accumulator.
+// and a lo plane (about 16 significant bits), stacked into one N = 2 nb operand
+// whose two accumulator halves are added when they are drained.
 //
 // Per 64-token stage: TMA brings the codes [64 t][128 k] and the dU^T planes
-// [nb j][64 t]; eight warps turn the codes into the MN-major, 128-byte swizzled
-// BF16 tile the MMA reads (two boxes of 64 features) and the planes into the
-// scaled planes; one thread issues the MMAs.  The tokens are split over the
-// CTAs of a cluster, which sum their FP32 tiles in split order through
-// distributed shared memory.
+// [nb j][64 t], one warp the 64 scales; eight warps turn the codes into the
+// MN-major, 128-byte swizzled BF16 tile the MMA reads (two boxes of 64
+// features) and the planes into the scaled planes; one thread issues the MMAs.
+// The tokens are split over the CTAs of a cluster, which sum their FP32 tiles
+// in split order through distributed shared memory.
 //
 // Launched after the dX GEMM as a programmatic dependent whose inputs were all
 // complete before that GEMM started: it runs on the SMs the GEMM's last round
-// leaves idle and waits for it only before it exits.
+// leaves idle and waits for it only before it exits.  (In front of the GEMM it
+// took 2 us longer at 4096^3, and no less with the codes brought to L2 during
+// the launch before.)
 //
 // Warps: 0 TMA producer, 1 tensor-memory allocation + MMA issue, 2-9
-// conversion; 2-5 also the epilogue.
+// conversion (2-5 also the epilogue), 10 the scales.
 
 #include "common.cuh"
 #include "gemm_common.cuh"
@@ -44,15 +47,17 @@ constexpr int kConvStages = 2;
 constexpr int kMaxRaw = 6;
 constexpr int kConvWarps = 8;
 constexpr int kConvThreads = 32 * kConvWarps;
-constexpr int kThreads = 64 + kConvThreads;
+constexpr int kThreads = 64 + kConvThreads + 32;
 // raw full/empty, conv full/empty, accumulator, tensor-memory slot
 constexpr int kBarBytes = 8 * (2 * kMaxRaw + 2 * kConvStages + 1) + 8;
 constexpr int kFixed = kBarBytes + 1024;
 constexpr int kPitch = AM + 4;
-constexpr int kMaxSmem = 220 * 1024;
+constexpr int kMaxSmem = 224 * 1024;
 constexpr int kMaxSplits = 8;
 
-int raw_stage_bytes(int nb) { return RAW_X + 2 * nb * AT * 2; }
+constexpr int SC_BYTES = AT * 4;              // one stage's scales
+
+int raw_stage_bytes(int nb) { return RAW_X + 2 * nb * AT * 2 + SC_BYTES; }
 int conv_stage_bytes(int nb) { return CONV_X + 2 * nb * AT * 2; }
 
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
@@ -90,21 +95,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   constexpr uint32_t Q_BYTES = NB * AT * 2;                  // one plane [NB j][64 t]
   constexpr uint32_t RAW = RAW_X + 2 * Q_BYTES, CONV = CONV_X + 2 * Q_BYTES;
-  constexpr uint32_t TMEM_COLS = NB < 32 ? 32u : static_cast<uint32_t>(NB);
+  constexpr uint32_t TMEM_COLS = 2 * NB;
   constexpr int CW = NB < 32 ? 16 : 32;
   constexpr int Q_ITEMS = NB * 8;                            // (j, 8-token chunk) pairs of a stage
   constexpr int Q_ITER = (Q_ITEMS + kConvThreads - 1) / kConvThreads;
   const int NR = a.raw_stages;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t raw0 = base + kConvStages * CONV;
-  const uint32_t bar0 = raw0 + static_cast<uint32_t>(NR) * RAW;
+  const uint32_t sc0 = raw0 + static_cast<uint32_t>(NR) * RAW;
+  const uint32_t bar0 = sc0 + static_cast<uint32_t>(NR) * SC_BYTES;
   // the swizzled planes of a stage come first: whole 1 KiB atoms
-  auto raw_q = [&](int s, int p) { return raw0 + static_cast<uint32_t>(s) * RAW + static_cast<uint32_t>(p) * Q_BYTES; };
+  auto raw_q = [&](int s) { return raw0 + static_cast<uint32_t>(s) * RAW; };
   auto raw_x = [&](int s) { return raw0 + static_cast<uint32_t>(s) * RAW + 2 * Q_BYTES; };
+  auto raw_sc = [&](int s) { return sc0 + static_cast<uint32_t>(s) * SC_BYTES; };
   auto conv_x = [&](int s) { return base + static_cast<uint32_t>(s) * CONV; };
-  auto conv_q = [&](int s, int p) {
-    return base + static_cast<uint32_t>(s) * CONV + CONV_X + static_cast<uint32_t>(p) * Q_BYTES;
-  };
+  auto conv_q = [&](int s) { return base + static_cast<uint32_t>(s) * CONV + CONV_X; };
   auto rfull = [&](int s) { return bar0 + 8u * s; };
   auto rempty = [&](int s) { return bar0 + 8u * (kMaxRaw + s); };
   auto cfull = [&](int s) { return bar0 + 8u * (2 * kMaxRaw + s); };
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int s = 0; s < NR; ++s) {
-      mbar_init(rfull(s), 1);
+      mbar_init(rfull(s), 2);   // the TMA producer and the scales' warp
       mbar_init(rempty(s), kConvWarps);
     }
     for (int s = 0; s < kConvStages; ++s) {
@@ -152,19 +157,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
-      int issued = 0;
+      int issued = 0, s = 0;
+      uint32_t ph = 1;
       for (int st = 0; st < nst; ++st) {
-        const int s = st % NR;
-        if (s_abort || !mbar_wait(rempty(s), ((st / NR) & 1) ^ 1, a.status)) {
+        if (s_abort || !mbar_wait_spin(rempty(s), ph, a.status)) {
           s_abort = 1;
           break;
         }
         const int32_t t = static_cast<int32_t>(tbeg + static_cast<int64_t>(st) * AT);
         mbar_arrive_expect_tx(rfull(s), RAW);
         tma_load_2d(raw_x(s), &tm_x, rfull(s), static_cast<int32_t>(k0), t);   // [64 t][128 k]
-        tma_load_2d(raw_q(s, 0), &tm_hi, rfull(s), t, 0);                      // [NB j][64 t]
-        tma_load_2d(raw_q(s, 1), &tm_lo, rfull(s), t, 0);
+        tma_load_2d(raw_q(s), &tm_hi, rfull(s), t, 0);                         // [NB j][64 t]
+        tma_load_2d(raw_q(s) + Q_BYTES, &tm_lo, rfull(s), t, 0);
         issued = st + 1;
+        if (++s == NR) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
       if (s_abort)
         for (int st = max(0, issued - NR); st < issued; ++st) mbar_wait(rfull(st % NR), (st / NR) & 1, a.status);
@@ -173,92 +182,119 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
     if (elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16_f32(AM, NB, true, false);
+      constexpr uint32_t idesc = idesc_bf16_f32(AM, 2 * NB, true, false);
       bool ok = true;
       for (int st = 0; st < nst; ++st) {
         const int s = st % kConvStages;
-        if (!mbar_wait(cfull(s), (st / kConvStages) & 1, a.status)) {
+        if (!mbar_wait_spin(cfull(s), (st / kConvStages) & 1, a.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t ad = smem_desc_sw128(conv_x(s) + kk * 2048, CONV_X / 2, 1024);
-          for (int p = 0; p < 2; ++p)
-            tc_mma_ss(tmem, ad, smem_desc_sw128(conv_q(s, p) + kk * 32, 16, 1024), idesc,
-                      (st > 0 || kk > 0 || p > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_ss(tmem, smem_desc_sw128(conv_x(s) + kk * 2048, CONV_X / 2, 1024),
+                    smem_desc_sw128(conv_q(s) + kk * 32, 16, 1024), idesc, (st > 0 || kk > 0) ? 1u : 0u);
         tc_commit(cempty(s));
       }
       if (!ok) s_abort = 1;
       tc_commit(acc_bar);   // also drains: arrives once everything issued has completed
     }
     __syncwarp();
+  } else if (warp == 2 + kConvWarps) {
+    // ---------------- the scales, loaded four stages ahead ----------------
+    const float *sg = a.scales + (a.grouped ? static_cast<int64_t>(blockIdx.x) * a.T : 0);
+    float2 r[4];
+    auto load = [&](int st, float2 &v) {
+      const int64_t t = tbeg + static_cast<int64_t>(st) * AT + lane;
+      v.x = st < nst && t < tend ? __ldg(sg + t) : 0.f;
+      v.y = st < nst && t + 32 < tend ? __ldg(sg + t + 32) : 0.f;
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load(i, r[i]);
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int st0 = 0; st0 < nst && ok; st0 += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (ok && st0 + i < nst) {
+          ok = __all_sync(0xffffffffu, !s_abort && mbar_wait(rempty(s), ph, a.status));
+          if (ok) {
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(raw_sc(s) + 4u * lane), "f"(r[i].x) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(raw_sc(s) + 4u * lane + 128u), "f"(r[i].y) : "memory");
+            load(st0 + i + 4, r[i]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(rfull(s));
+            if (++s == NR) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+      }
+    }
+    if (!ok) s_abort = 1;
   } else {
     // ---------------- conversion ----------------
     const int ct = static_cast<int>(threadIdx.x) - 64;
-    const float *sg = a.scales + (a.grouped ? static_cast<int64_t>(blockIdx.x) * a.T : 0);
-    const int ch = ct & 7;   // this thread's 8-token chunk of the planes
-    const bool has_q = ct < Q_ITEMS;
-    float sc[8];
-    auto load_scales = [&](int st) {
-      const int64_t t = tbeg + static_cast<int64_t>(st) * AT + ch * 8;
+    // The codes: 16 features of one token per item, two items a thread.  A
+    // warp takes eight tokens; eight lanes (a quarter of a shared-memory
+    // access) take four 16-feature chunks of one box for two tokens whose
+    // numbers differ by 5 in exclusive or: with both swizzles, their reads and
+    // their writes then fall in different 16-byte bank groups.
+    uint32_t xr[2], xw0[2], xw1[2];   // offsets: the item read, its two 16-byte halves written
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sc[e] = has_q && st < nst && t + e < tend ? __ldg(sg + t + e) : 0.f;
-    };
-    load_scales(0);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t c = lane & 3u, h = (lane >> 3) & 1u, p = 2u * i + (lane >> 4);
+      const uint32_t x = (lane & 4u) ? p ^ 5u : p;               // token of the warp's eight
+      const uint32_t row = static_cast<uint32_t>(warp - 2) * 1024u + x * 128u;
+      xr[i] = row + (((4u * h + c) ^ x) << 4);
+      xw0[i] = h * (CONV_X / 2) + row + (((2u * c) ^ x) << 4);
+      xw1[i] = h * (CONV_X / 2) + row + (((2u * c + 1u) ^ x) << 4);
+    }
+    const uint32_t ch = ct & 7u;   // this thread's 8-token chunk of the planes
+    int rs = 0, cs = 0;
+    uint32_t rph = 0, cph = 1;
     for (int st = 0; st < nst; ++st) {
-      const int rs = st % NR, cs = st % kConvStages;
-      bool ok = !s_abort && mbar_wait(rfull(rs), (st / NR) & 1, a.status);
-      ok = ok && mbar_wait(cempty(cs), ((st / kConvStages) & 1) ^ 1, a.status);
+      bool ok = !s_abort && mbar_wait(rfull(rs), rph, a.status);
+      ok = ok && mbar_wait(cempty(cs), cph, a.status);
       if (!__all_sync(0xffffffffu, ok)) {
         s_abort = 1;
         break;
       }
-      // the codes: 16 features of one token per item
+      const uint32_t src = raw_x(rs), dst = conv_x(cs);
+      uint4 q[2];
 #pragma unroll
-      for (int i = 0; i < AT * 8 / kConvThreads; ++i) {
-        const int it = i * kConvThreads + ct;
-        const int t = it >> 3, c16 = it & 7;
-        const uint4 q = ld_shared_v4(raw_x(rs) + static_cast<uint32_t>(t * 128) + (static_cast<uint32_t>(c16 ^ (t & 7)) << 4));
-        const int h = c16 >> 2;   // box of 64 features
-        const uint32_t row = conv_x(cs) + static_cast<uint32_t>(h * (CONV_X / 2) + t * 128);
-        const uint32_t lo[4] = {bytes_to_bf16x2(q.x, 0x4140u), bytes_to_bf16x2(q.x, 0x4342u),
-                                bytes_to_bf16x2(q.y, 0x4140u), bytes_to_bf16x2(q.y, 0x4342u)};
-        const uint32_t hi[4] = {bytes_to_bf16x2(q.z, 0x4140u), bytes_to_bf16x2(q.z, 0x4342u),
-                                bytes_to_bf16x2(q.w, 0x4140u), bytes_to_bf16x2(q.w, 0x4342u)};
-        const uint32_t c = static_cast<uint32_t>((c16 & 3) * 2), x = static_cast<uint32_t>(t & 7);
-        // the two boxes write their two chunks in opposite order: eight lanes
-        // of a token then cover eight different 16-byte bank groups
-        if (h == 0) {
-          st_shared_v4(row + ((c ^ x) << 4), lo[0], lo[1], lo[2], lo[3]);
-          st_shared_v4(row + (((c + 1) ^ x) << 4), hi[0], hi[1], hi[2], hi[3]);
-        } else {
-          st_shared_v4(row + (((c + 1) ^ x) << 4), hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(row + ((c ^ x) << 4), lo[0], lo[1], lo[2], lo[3]);
-        }
+      for (int i = 0; i < 2; ++i) q[i] = ld_shared_v4(src + xr[i]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        st_shared_v4(dst + xw0[i], bytes_to_bf16x2(q[i].x, 0x4140u), bytes_to_bf16x2(q[i].x, 0x4342u),
+                     bytes_to_bf16x2(q[i].y, 0x4140u), bytes_to_bf16x2(q[i].y, 0x4342u));
+        st_shared_v4(dst + xw1[i], bytes_to_bf16x2(q[i].z, 0x4140u), bytes_to_bf16x2(q[i].z, 0x4342u),
+                     bytes_to_bf16x2(q[i].w, 0x4140u), bytes_to_bf16x2(q[i].w, 0x4342u));
       }
       // the planes: eight tokens of one column j per item
+      if (ct < Q_ITEMS) {
+        const uint4 s0 = ld_shared_v4(raw_sc(rs) + ch * 32u), s1 = ld_shared_v4(raw_sc(rs) + ch * 32u + 16u);
+        const uint32_t sc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-      for (int i = 0; i < Q_ITER; ++i) {
-        const int it = i * kConvThreads + ct;
-        if (it < Q_ITEMS) {
-          const int j = it >> 3;
-          const uint32_t off = static_cast<uint32_t>(j * 128) + ((static_cast<uint32_t>(ch) ^ (j & 7u)) << 4);
-          const uint4 hv = ld_shared_v4(raw_q(rs, 0) + off), lv = ld_shared_v4(raw_q(rs, 1) + off);
+        for (int i = 0; i < Q_ITER; ++i) {
+          const uint32_t j = static_cast<uint32_t>(ct >> 3) + i * (kConvThreads / 8);
+          const uint32_t off = j * 128u + ((ch ^ (j & 7u)) << 4);
+          const uint4 hv = ld_shared_v4(raw_q(rs) + off), lv = ld_shared_v4(raw_q(rs) + Q_BYTES + off);
           const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w};
           uint32_t oh[4], ol[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float v0 = (__uint_as_float(hw[e] << 16) + __uint_as_float(lw[e] << 16)) * sc[2 * e];
-            const float v1 = (__uint_as_float(hw[e] & 0xFFFF0000u) + __uint_as_float(lw[e] & 0xFFFF0000u)) * sc[2 * e + 1];
-            const __nv_bfloat162 hh = __floats2bfloat162_rn(v0, v1);
-            oh[e] = *reinterpret_cast<const uint32_t *>(&hh);
-            ol[e] = pack_bf16x2(v0 - __low2float(hh), v1 - __high2float(hh));
+            const float v0 = (__uint_as_float(hw[e] << 16) + __uint_as_float(lw[e] << 16)) * __uint_as_float(sc[2 * e]);
+            const float v1 = (__uint_as_float(hw[e] & 0xFFFF0000u) + __uint_as_float(lw[e] & 0xFFFF0000u)) *
+                             __uint_as_float(sc[2 * e + 1]);
+            oh[e] = pack_bf16x2(v0, v1);
+            ol[e] = pack_bf16x2(v0 - __uint_as_float(oh[e] << 16), v1 - __uint_as_float(oh[e] & 0xFFFF0000u));
           }
-          st_shared_v4(conv_q(cs, 0) + off, oh[0], oh[1], oh[2], oh[3]);
-          st_shared_v4(conv_q(cs, 1) + off, ol[0], ol[1], ol[2], ol[3]);
+          st_shared_v4(conv_q(cs) + off, oh[0], oh[1], oh[2], oh[3]);
+          st_shared_v4(conv_q(cs) + Q_BYTES + off, ol[0], ol[1], ol[2], ol[3]);
         }
       }
       fence_proxy_async_smem();
@@ -267,7 +303,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(rempty(rs));
         mbar_arrive(cfull(cs));
       }
-      load_scales(st + 1);
+      if (++rs == NR) {
+        rs = 0;
+        rph ^= 1u;
+      }
+      if (++cs == kConvStages) {
+        cs = 0;
+        cph ^= 1u;
+      }
     }
     if (warp < 6) {
       // ---------------- the FP32 tile to shared memory, column j by column j ----------------
@@ -276,25 +319,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool fail = !mbar_wait(acc_bar, 0, a.status) || s_abort;
       const bool have = __all_sync(0xffffffffu, !fail);   // tcgen05.ld is warp-collective
       tc_fence_after();
-      // (every warp has left the conversion loop: the accumulator is complete
-      // only after the last conversion, and the ring is drained)
+      // (the accumulator is complete only after the last conversion: no warp
+      // reads or writes the rings any more)
       const uint32_t trow = tmem + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
       for (int c0 = 0; c0 < a.R; c0 += CW) {
-        uint32_t v[CW];
+        uint32_t v[CW], w[CW];
         if (have) {
-          if constexpr (CW == 16) tmem_ld_32x32b_x16(trow + c0, v);
-          else tmem_ld_32x32b_x32(trow + c0, v);
+          if constexpr (CW == 16) {
+            tmem_ld_32x32b_x16(trow + c0, v);
+            tmem_ld_32x32b_x16(trow + NB + c0, w);
+          } else {
+            tmem_ld_32x32b_x32(trow + c0, v);
+            tmem_ld_32x32b_x32(trow + NB + c0, w);
+          }
           tc_wait_ld();
+          reg_fence(v);
+          reg_fence(w);
         } else {
 #pragma unroll
-          for (int j = 0; j < CW; ++j) v[j] = 0u;
+          for (int j = 0; j < CW; ++j) v[j] = w[j] = 0u;
         }
 #pragma unroll
         for (int j = 0; j < CW; ++j)
           if (c0 + j < a.R)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + static_cast<uint32_t>((c0 + j) * kPitch + row) * 4u),
-                         "r"(v[j])
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + static_cast<uint32_t>((c0 + j) * kPitch + row) * 4u),
+                         "f"(__uint_as_float(v[j]) + __uint_as_float(w[j]))
                          : "memory");
       }
     }
@@ -327,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   // no CTA leaves (and frees its shared memory) while another still reads it
-  if (splits > 1) cluster_arrive_wait();
+  if (splits > 1) cluster_arrive_wait_relaxed();
   else __syncthreads();
   grid_dep_wait();
   if (warp == 1) {
@@ -348,11 +398,11 @@ DaInt8Geom da_int8_geom(int64_t T, int64_t K, int r, int num_sms) {
   }
   if (g.raw_stages > kMaxRaw) g.raw_stages = kMaxRaw;
   g.smem = conv + g.raw_stages * raw_stage_bytes(g.nb);
+  // one wave of CTAs, at least four stages a split; a power of two, so that
+  // clusters fill the GPU's partitions
   const int64_t tiles = (K + AM - 1) / AM, steps = (T + AT - 1) / AT;
-  int64_t s = static_cast<int64_t>(per_sm) * num_sms / tiles;
-  if (s > kMaxSplits) s = kMaxSplits;
-  if (s > (steps + 1) / 2) s = (steps + 1) / 2;   // at least two stages a split
-  if (s < 1) s = 1;
+  int64_t s = 1;
+  while (2 * s <= kMaxSplits && 2 * s * tiles <= per_sm * static_cast<int64_t>(num_sms) && steps >= 8 * s) s *= 2;
   g.t_per_split = (steps + s - 1) / s * AT;
   g.splits = static_cast<int>((T + g.t_per_split - 1) / g.t_per_split);
   return g;

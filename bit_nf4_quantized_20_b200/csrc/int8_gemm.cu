@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads)
   int8::join_splits(base, splits, split, 1u, 0u, tv, t0, n0, a.N, a.sx, a.sw, a.y);
   __syncwarp();
   // no CTA leaves (and frees its shared memory) while another still reads it
-  if (splits > 1) cluster_arrive_wait();
+  if (splits > 1) cluster_arrive_wait_relaxed();
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
