@@ -412,9 +412,10 @@ _INT8_GROUP = 128
 class QuantizedInt8:
     """A matrix in signed 8-bit codes (qlora_int8_matrix): value = code * scale,
     one FP32 scale per row (group 0) or per 128 consecutive columns of a row
-    (group 128).  codes: int8 [rows, cols]; scales: float32 [groups, rows]."""
+    (group 128).  codes: int8 [rows, cols]; scales: float32 [groups, rows]; the
+    attributes are read-only (the buffers' contents are not)."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "group", "device", "_struct", "_ref")
+    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_group", "_device", "_struct", "_ref")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, group: int = 0):
         _need_cuda("codes", codes, dtype=torch.int8)
@@ -432,8 +433,8 @@ class QuantizedInt8:
         self._set(codes, scales, rows, cols, group, codes.device)
 
     def _set(self, codes, scales, rows, cols, group, device):
-        self.codes, self.scales, self.rows, self.cols, self.group = codes, scales, rows, cols, group
-        self.device = device
+        self._codes, self._scales, self._rows, self._cols, self._group = codes, scales, rows, cols, group
+        self._device = device
         self._struct = _lib.Int8Matrix(codes.data_ptr(), scales.data_ptr(), rows, cols, group)
         self._ref = C.byref(self._struct)
         _status(device)   # before any capture
@@ -445,8 +446,18 @@ class QuantizedInt8:
         self._set(*args)
         return self
 
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    group = property(lambda self: self._group)
+    device = property(lambda self: self._device)
+
+    def __reduce__(self):
+        return QuantizedInt8, (self._codes, self._scales, self._group)
+
     def nbytes(self) -> int:
-        return self.codes.numel() + 4 * self.scales.numel()
+        return self._codes.numel() + 4 * self._scales.numel()
 
 
 # the current stream's handle by device index, without a Stream object (2 us less a call)

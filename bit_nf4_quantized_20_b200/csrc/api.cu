@@ -1354,6 +1354,8 @@ static qlora_status check_linear_int8(int64_t T, int64_t K, const qlora_int8_mat
   if (T < 0 || w->rows <= 0 || w->cols != K || (T > 0 && !y)) return QLORA_ERR_INVALID_ARG;
   // INT32 sums of K products of at most 127 x 127; Y's rows start on 16 bytes
   if (w->group != 0 || w->rows % 8 != 0 || K > QLORA_INT8_MAX_K || T > QLORA_INT8_MAX_T) return QLORA_ERR_UNSUPPORTED;
+  // (the tiles of the pair variant are numbered in 31 bits)
+  if ((w->rows + 255) / 256 * ((T + 127) / 128) > 0x3fffffff) return QLORA_ERR_UNSUPPORTED;
   if (!aligned16(y) || (reinterpret_cast<uintptr_t>(status) & 3u)) return QLORA_ERR_MISALIGNED;
   return QLORA_OK;
 }

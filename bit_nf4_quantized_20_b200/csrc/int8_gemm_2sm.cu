@@ -382,7 +382,7 @@ cudaError_t launch_int8_gemm_2sm(const Int8PairArgs &args, const CUtensorMap &tm
   Int8PairArgs p = args;
   if (p.T <= 0 || p.N <= 0 || p.K <= 0 || p.N % 8 != 0) return cudaErrorInvalidValue;
   p.ksteps = static_cast<int>((p.K + KB - 1) / KB);
-  if ((p.N + 2 * PM - 1) / (2 * PM) * ((p.T + HN - 1) / HN) > 0x3fffffff) return cudaErrorInvalidValue;
+  if ((p.N + 2 * PM - 1) / (2 * PM) * ((p.T + HN - 1) / HN) > 0x3fffffff) return cudaErrorInvalidValue;   // int units
   p.units = int8_pair_units(p.T, p.N, num_sms);
   const int64_t units = p.units.full + static_cast<int64_t>(p.units.halves), pairs = num_sms / 2;
   const int64_t clusters = units < pairs ? units : pairs;

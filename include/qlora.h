@@ -389,7 +389,8 @@ QLORA_API qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *o
  * qlora_linear_int8_q takes an already quantized x (group 0), so that several
  * products can share one.  y[T, N]: BF16, 16-byte aligned.  Results do not
  * depend on timing.  N % 8 == 0, K % 16 == 0, K <= QLORA_INT8_MAX_K (the INT32
- * sums stay exact), T <= QLORA_INT8_MAX_T; T == 0 is a no-op.
+ * sums stay exact), T <= QLORA_INT8_MAX_T (and T * N below 2^45); T == 0 is a
+ * no-op.
  * scratch: qlora_linear_int8_scratch_bytes(T, K) bytes (0 on invalid
  * arguments), 16-byte aligned; it need not be initialised and holds nothing
  * between calls, but calls that may overlap must not share it.

@@ -172,6 +172,7 @@ def test_linear_int8_validation(L):
     assert call(w=matrix(rows=64, cols=256, group=128)) == 2  # one scale per output channel
     assert call(w=matrix(rows=64, cols=131072 + 16)) == 2     # INT32 sums
     assert call(T=65535 * 256 + 1) == 2
+    assert call(T=65535 * 256, w=matrix(rows=1 << 30, cols=16)) == 2   # more tiles than the kernels count
     assert call(x=P + 2) == 3
     assert call(y=P + 8) == 3
     assert call(status=P + 1) == 3

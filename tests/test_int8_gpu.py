@@ -393,6 +393,60 @@ def test_captured_replayed_and_interleaved():
     del graphs
 
 
+def test_random_shapes():
+    """Sizes drawn over the whole range, each operator: bit-exact codes, values
+    and products, bounded gradients."""
+    import random
+    rng = random.Random(20)
+    log = lambda lo, hi, m: max(m, int(round(np.exp(rng.uniform(np.log(lo), np.log(hi))))) // m * m)
+    for _ in range(25):
+        check_quantize(activation(log(1, 3000, 1), log(16, 9000, 16), rng.randrange(1 << 20)), rng.choice((0, 128)))
+        T, N, K = log(1, 3000, 1), log(8, 3000, 8), log(16, 6000, 16)
+        check_linear(activation(T, K, rng.randrange(1 << 20)),
+                     inputs.normal_bf16((N, K), 0.02, rng.randrange(1 << 20), "cuda"))
+    for _ in range(8):
+        check_backward(log(1, 1500, 1), log(8, 1000, 8), log(64, 3000, 64), rng.randint(1, 128), 1.0,
+                       rng.choice((0, 128)))
+
+
+def test_scratch_and_workspace_need_no_initialisation():
+    """The per-call buffers come from the allocator as they are: all ones here
+    (NaN, and every counter and flag set)."""
+    q = Q()
+    for r in (16, 100):
+        W, X, A, B, dY = layer(300, 520, 640, r, 2.0)
+        qw, w8 = q.quantize_nf4(W), q.quantize_int8(W)
+        _, u = q.linear_fwd_save(X, qw, A, B, 2.0)
+        x8 = q.quantize_int8(X, group=128)
+        first = (q.linear_int8(X, w8), *q.linear_bwd_saved_int8(dY, x8, qw, A, B, 2.0, u))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 16, 1 << 20, 1 << 22, 1 << 24)]
+            del junk
+            again = (q.linear_int8(X, w8), *q.linear_bwd_saved_int8(dY, x8, qw, A, B, 2.0, u))
+            assert all(equal_bits(a, b) for a, b in zip(first, again))
+    q.get_error()
+
+
+def test_quantized_int8_object():
+    import io
+    q = Q()
+    x8 = q.quantize_int8(activation(5, 272, 1), group=128)
+    with pytest.raises(AttributeError):
+        x8.codes = torch.zeros(5, 272, dtype=torch.int8, device="cuda")
+    assert x8.nbytes() == 5 * 272 + 4 * 3 * 5
+    f = io.BytesIO()
+    torch.save(x8, f)
+    f.seek(0)
+    y8 = torch.load(f, weights_only=False)
+    assert torch.equal(y8.codes, x8.codes) and torch.equal(y8.scales, x8.scales) and y8.group == 128
+    assert equal_bits(q.dequantize_int8(y8), q.dequantize_int8(x8))
+    for bad in (dict(scales=torch.zeros(1, 5, device="cuda")), dict(codes=torch.zeros(5, 272, device="cuda")),
+                dict(codes=x8.codes.t()), dict(group=64)):
+        with pytest.raises(ValueError):
+            q.QuantizedInt8(**{**dict(codes=x8.codes, scales=x8.scales, group=128), **bad})
+
+
 def test_two_streams_at_once():
     """The same weight and the same token batch from two streams at once."""
     q = Q()
