@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -519,6 +520,11 @@ def dequantize_int8(q8: QuantizedInt8, out: torch.Tensor | None = None) -> torch
     return out
 
 
+@lru_cache(maxsize=4096)
+def _int8_scratch_bytes(T: int, N: int, K: int) -> int:
+    return int(lib().qlora_linear_int8_scratch_bytes(T, N, K))
+
+
 def linear_int8(x, w8: QuantizedInt8, out: torch.Tensor | None = None) -> torch.Tensor:
     """y = xq wq^T (BF16): the INT32 product of 8-bit codes, scaled per token
     and per output channel.  x: BF16 [T, K], quantized per token in the call,
@@ -547,13 +553,12 @@ def linear_int8(x, w8: QuantizedInt8, out: torch.Tensor | None = None) -> torch.
     if given:
         _int8_call(dev, "qlora_linear_int8_q", x._ref, w8._ref, out.data_ptr(), _status(dev))
     else:
-        # the quantized tokens live for this call only (the allocator hands the
-        # block to work that follows on this stream, or keeps it in the pool of
-        # the graph being captured)
-        n = lib().qlora_linear_int8_scratch_bytes(T, K)
-        scratch = torch.empty(n, dtype=torch.uint8, device=dev)
-        _int8_call(dev, "qlora_linear_int8", x.data_ptr(), T, w8._ref, out.data_ptr(), scratch.data_ptr(), n,
-                   _status(dev))
+        # the quantized tokens, where they need memory, live for this call only
+        # (the allocator hands the block to work that follows on this stream, or
+        # keeps it in the pool of the graph being captured)
+        n = _int8_scratch_bytes(T, w8._rows, K)
+        scratch = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        _int8_call(dev, "qlora_linear_int8", x.data_ptr(), T, w8._ref, out.data_ptr(), _ptr(scratch), n, _status(dev))
     return out
 
 

@@ -94,7 +94,7 @@ SIGNATURES = {
                                            C.POINTER(C.c_size_t)]),
     "qlora_quantize_int8": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_int32, C.POINTER(Int8Matrix), C.c_void_p]),
     "qlora_dequantize_int8": (C.c_int, [C.POINTER(Int8Matrix), C.c_void_p, C.c_void_p]),
-    "qlora_linear_int8_scratch_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
+    "qlora_linear_int8_scratch_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64]),
     "qlora_linear_int8": (C.c_int, [C.c_void_p, C.c_int64, C.POINTER(Int8Matrix), C.c_void_p, C.c_void_p, C.c_size_t,
                                     C.c_void_p, C.c_void_p]),
     "qlora_linear_int8_q": (C.c_int, [C.POINTER(Int8Matrix), C.POINTER(Int8Matrix), C.c_void_p, C.c_void_p,

@@ -74,14 +74,16 @@ enum KernelId : int32_t {
   K_DEQUANTIZE_INT8 = 17,
   K_INT8_GEMM = 18,
   K_DA_INT8 = 19,       // dA from an 8-bit activation
-  K_COUNT = 20,
+  K_INT8_DECODE = 20,   // int8 product of a few tokens, quantized in the launch
+  K_COUNT = 21,
 };
 
 const char *kKernelNames[K_COUNT] = {"quantize_nf4_dq", "dequantize_nf4", "lora_u",       "lora_du",
                                      "lora_dB",         "lora_dA",        "nf4_gemm_fwd", "nf4_gemm_bwd_dx",
                                      "nf4_gemv_fwd",    "lora_u+du",      "lora_dB+dA",   "merge_adapter",
                                      "lora_du+dB",      "adam_step",      "lora_du+dB_sum", "unknown",      "quantize_int8",
-                                     "dequantize_int8", "int8_gemm",      "lora_dA_int8"};
+                                     "dequantize_int8", "int8_gemm",      "lora_dA_int8",
+                                     "int8_decode"};
 
 struct TraceScope {
   cudaStream_t st;
@@ -117,8 +119,8 @@ int num_sms_current() {
   return cache[dev];
 }
 
-// Splits of the rank-r GEMMs are sized for a fixed CTA target so that the
-// workspace size does not depend on the device.
+// Splits of the rank-r GEMMs and of the int8 products are sized for a fixed CTA
+// target so that workspace sizes (and variants) do not depend on the device.
 constexpr int kSplitSms = 148;
 
 // ---------------------------------------------------------------------------
@@ -1372,7 +1374,7 @@ struct Int8Launch {
 static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, const qlora_int8_matrix *w, void *y,
                                  void *status, bool early, Int8Launch &l) {
   const int64_t N = w->rows, K = w->cols;
-  l.g = int8_gemm_geom(T, N, K, num_sms_current());
+  l.g = int8_gemm_geom(T, N, K, kSplitSms);
   memset(&l.a, 0, sizeof(l.a));
   memset(&l.p, 0, sizeof(l.p));
   l.a.T = T;
@@ -1409,8 +1411,10 @@ static qlora_status launch_int8(const Int8Launch &l, cudaStream_t st) {
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-size_t qlora_linear_int8_scratch_bytes(int64_t T, int64_t K) {
-  if (T < 0 || T > QLORA_INT8_MAX_T || K <= 0 || K > QLORA_INT8_MAX_K || K % 16 != 0) return 0;
+size_t qlora_linear_int8_scratch_bytes(int64_t T, int64_t N, int64_t K) {
+  if (T < 0 || T > QLORA_INT8_MAX_T || N <= 0 || N % 8 != 0 || K <= 0 || K > QLORA_INT8_MAX_K || K % 16 != 0) return 0;
+  Int8DecodeGeom g;
+  if (int8_decode_geom(T, N, K, kSplitSms, g)) return 0;   // quantized inside the product
   return static_cast<size_t>(round_up(T * K, 256) + round_up(T * 4, 256));
 }
 
@@ -1421,15 +1425,34 @@ qlora_status qlora_linear_int8(const void *x_bf16, int64_t T, const qlora_int8_m
   if (T == 0) return QLORA_OK;
   if (!x_bf16) return QLORA_ERR_INVALID_ARG;
   if (!aligned16(x_bf16)) return QLORA_ERR_MISALIGNED;
-  const int64_t K = w->cols;
-  if (!scratch || !aligned16(scratch) || scratch_bytes < qlora_linear_int8_scratch_bytes(T, K))
+  const int64_t N = w->rows, K = w->cols;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Int8DecodeGeom g;
+  if (int8_decode_geom(T, N, K, kSplitSms, g)) {
+    Int8DecodeArgs a;
+    memset(&a, 0, sizeof(a));
+    a.T = static_cast<int>(T);
+    a.N = N;
+    a.K = K;
+    a.x = static_cast<const uint16_t *>(x_bf16);
+    a.sw = w->scales;
+    a.y = static_cast<uint16_t *>(y);
+    a.stages = g.stages;
+    a.kb_per_split = g.kb_per_split;
+    a.status = static_cast<uint32_t *>(status);
+    CUtensorMap m_w;
+    if (!make_map_u8(&m_w, w->codes, N, K, K, 128, 128)) return QLORA_ERR_CUDA;
+    const double n = static_cast<double>(N), k = static_cast<double>(K);
+    TraceScope ts(K_INT8_DECODE, 2.0 * T * n * k, n * k + 4.0 * n + 2.0 * T * (n + k), st);
+    return launch_int8_decode(a, g, m_w, st, g_trace.recs == nullptr) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  }
+  if (!scratch || !aligned16(scratch) || scratch_bytes < qlora_linear_int8_scratch_bytes(T, N, K))
     return QLORA_ERR_WORKSPACE;
   int8_t *xq = static_cast<int8_t *>(scratch);
   float *sx = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + round_up(T * K, 256));
   Int8Launch l;
   cs = prepare_int8(xq, sx, T, w, y, status, true, l);
   if (cs != QLORA_OK) return cs;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   cs = run_quantize_int8(x_bf16, T, K, 0, xq, sx, st);
   if (cs != QLORA_OK) return cs;
   return launch_int8(l, st);

@@ -20,54 +20,14 @@
 // Both kernels move each byte once (2 + 1 bytes an element in, 1 + 2 out):
 // bound by HBM for large matrices, by launch latency for a few rows.
 #include "common.cuh"
+#include "int8_common.cuh"
 #include "kernels.h"
 
 namespace qlora {
 
+using namespace int8;
+
 namespace {
-
-constexpr float kRoundMagic = 12582912.0f;   // 1.5 * 2^23
-constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
-
-// elementwise max over |bits| of eight BF16 values (BF16 order = magnitude order), as u16x2
-__device__ __forceinline__ uint32_t abs_max8(const uint4 &v) {
-  return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-}
-
-__device__ __forceinline__ uint32_t fold_u16x2(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
-
-struct RowScale {
-  float scale, inv;
-  bool bad;
-};
-
-__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
-  RowScale r;
-  r.bad = amax_bits >= 0x7F80u;
-  const float s = fmaxf(__fdiv_rn(__uint_as_float(amax_bits << 16), 127.0f), kMinScale);
-  r.scale = r.bad ? __uint_as_float(0x7FC00000u) : s;
-  r.inv = __frcp_rn(s);
-  return r;
-}
-
-// two BF16 values of a word -> the sums whose low bytes are their codes
-__device__ __forceinline__ uint32_t code_lo(uint32_t w, float inv) {
-  return __float_as_uint(__fmaf_rn(__uint_as_float(w << 16), inv, kRoundMagic));
-}
-__device__ __forceinline__ uint32_t code_hi(uint32_t w, float inv) {
-  return __float_as_uint(__fmaf_rn(__uint_as_float(w & 0xFFFF0000u), inv, kRoundMagic));
-}
-
-__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float inv) {
-  const uint32_t a = prmt(code_lo(w0, inv), code_hi(w0, inv), 0x0040);
-  const uint32_t b = prmt(code_lo(w1, inv), code_hi(w1, inv), 0x0040);
-  return prmt(a, b, 0x5410);
-}
-
-__device__ __forceinline__ uint2 codes8(const uint4 &v, const RowScale &r) {
-  if (r.bad) return make_uint2(0u, 0u);
-  return make_uint2(codes4(v.x, v.y, r.inv), codes4(v.z, v.w, r.inv));
-}
 
 // One scale a row.  A row is held in registers by THREADS threads, VPT 16-byte
 // loads each, so it is read once; the maximum crosses the warps of the row

@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kThreads)
   else __syncthreads();
 
   // this CTA's share of the tile
-  int8::join_splits(base, splits, split, 1u, 0u, tv, t0, n0, a.N, a.sx, a.sw, a.y);
+  const float *sx = a.sx + t0;
+  int8::join_splits<kThreads / 32>(base, splits, split, tv, t0, n0, a.N, [=](int t) { return __ldcg(sx + t); }, a.sw, a.y);
   __syncwarp();
   // no CTA leaves (and frees its shared memory) while another still reads it
   if (splits > 1) cluster_arrive_wait_relaxed();

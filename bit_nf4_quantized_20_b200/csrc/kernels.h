@@ -82,6 +82,24 @@ struct Int8GemmArgs {
 cudaError_t launch_int8_gemm(const Int8GemmArgs &a, const Int8GemmGeom &g, const CUtensorMap &tm_w,
                              const CUtensorMap &tm_x, cudaStream_t st, bool pdl);
 
+// The same for up to four tokens, quantized in the launch (int8_decode.cu)
+struct Int8DecodeGeom {
+  int stages, smem, splits, kb_per_split;   // as in Int8GemmGeom
+};
+// false: the size is not covered
+bool int8_decode_geom(int64_t T, int64_t N, int64_t K, int num_sms, Int8DecodeGeom &g);
+struct Int8DecodeArgs {
+  int T;
+  int64_t N, K;
+  const uint16_t *x;      // [T, K] BF16
+  const float *sw;        // [N]
+  uint16_t *y;            // [T, N] BF16
+  int stages, kb_per_split;
+  uint32_t *status;
+};
+// map: Wq [N rows, K bytes] box 128 x 128, 128-byte swizzle
+cudaError_t launch_int8_decode(const Int8DecodeArgs &a, const Int8DecodeGeom &g, const CUtensorMap &tm_w,
+                               cudaStream_t st, bool pdl);
 // The same product on CTA pairs, 256 x 256 tiles (int8_gemm_2sm.cu).  Work
 // units, dealt to the pairs in turn: full tiles first, then 128-token halves.
 struct Int8PairUnits {

@@ -391,9 +391,10 @@ QLORA_API qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *o
  * depend on timing.  N % 8 == 0, K % 16 == 0, K <= QLORA_INT8_MAX_K (the INT32
  * sums stay exact), T <= QLORA_INT8_MAX_T (and T * N below 2^45); T == 0 is a
  * no-op.
- * scratch: qlora_linear_int8_scratch_bytes(T, K) bytes (0 on invalid
- * arguments), 16-byte aligned; it need not be initialised and holds nothing
- * between calls, but calls that may overlap must not share it.
+ * scratch: qlora_linear_int8_scratch_bytes(T, N, K) bytes, 16-byte aligned (0
+ * on invalid arguments, and for one to four tokens where the product quantizes
+ * them itself: then scratch may be NULL); it need not be initialised and holds
+ * nothing between calls, but calls that may overlap must not share it.
  * status: a status word as at the start of a workspace (zeroed once, read by
  * qlora_get_error(status, stream)); any number of calls may share it; NULL: a
  * bounded wait that runs out is not reported.
@@ -401,7 +402,7 @@ QLORA_API qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *o
  */
 #define QLORA_INT8_MAX_K 131072
 #define QLORA_INT8_MAX_T (65535 * 256)
-QLORA_API size_t qlora_linear_int8_scratch_bytes(int64_t T, int64_t K);
+QLORA_API size_t qlora_linear_int8_scratch_bytes(int64_t T, int64_t N, int64_t K);
 QLORA_API qlora_status qlora_linear_int8(const void *x_bf16, int64_t T, const qlora_int8_matrix *w, void *y,
                                          void *scratch, size_t scratch_bytes, void *status, void *stream);
 QLORA_API qlora_status qlora_linear_int8_q(const qlora_int8_matrix *x, const qlora_int8_matrix *w, void *y,

@@ -177,13 +177,18 @@ def test_linear_int8_validation(L):
     assert call(y=P + 8) == 3
     assert call(status=P + 1) == 3
     assert call(w=matrix(rows=64, cols=256, codes=FAKE + 1)) == 3
-    assert call(scratch=None) == 4
-    assert call(scratch=P + 8) == 4
-    assert call(nbytes=5 * 256 - 1) == 4
+    assert call(T=17, scratch=None) == 4
+    assert call(T=17, scratch=P + 8) == 4
+    assert call(T=17, nbytes=17 * 256 + 255) == 4
     assert call(x=None, T=0, y=None, scratch=None, nbytes=0, status=None) == 0
     s = L.qlora_linear_int8_scratch_bytes
-    assert s(5, 256) == 1280 + 256
-    assert s(0, 256) == 0 and s(-1, 256) == 0 and s(5, 250) == 0 and s(5, 131088) == 0
+    assert s(17, 64, 256) == 17 * 256 + 256
+    assert s(4, 64, 256) == 0                                 # quantized inside the product
+    assert s(5, 64, 256) == 1280 + 256
+    assert s(4, 8, 131072) == 4 * 131072 + 256                # too long a range for that: 64 KiB of codes a CTA
+    assert s(1, 65536, 1024) == 1024 + 256                    # a long stream of weights
+    assert s(0, 64, 256) == 0 and s(-1, 64, 256) == 0 and s(17, 64, 250) == 0 and s(17, 64, 131088) == 0
+    assert s(17, 60, 256) == 0
     g = L.qlora_linear_int8_q
     x = matrix(rows=5, cols=256)
     assert g(None, C.byref(w), P, P, None) == 1
@@ -220,6 +225,7 @@ def test_kernel_names(L):
     assert L.qlora_kernel_name(17) == b"dequantize_int8"
     assert L.qlora_kernel_name(18) == b"int8_gemm"
     assert L.qlora_kernel_name(19) == b"lora_dA_int8"
+    assert L.qlora_kernel_name(20) == b"int8_decode"
 
 
 # --------------------------------------------------------------------------

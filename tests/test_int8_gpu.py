@@ -150,7 +150,8 @@ def check_linear(x, w):
 
 
 @pytest.mark.parametrize("T,N,K", [
-    (1, 8, 16), (1, 8, 128), (2, 136, 48), (1, 1024, 4096), (3, 40, 320), (15, 256, 144), (16, 512, 512),
+    (1, 8, 16), (1, 8, 128), (2, 136, 48), (1, 1024, 4096), (3, 40, 320), (4, 1032, 4112), (4, 4096, 4096), (1, 512, 14336),
+    (2, 24, 32784), (1, 8, 32768), (4, 16400, 1040), (5, 1024, 4096), (1, 14336, 4096), (15, 256, 144), (16, 512, 512),
     (17, 264, 1040), (31, 128, 2048), (32, 136, 4096), (33, 640, 256), (64, 1024, 272), (65, 248, 1024), (100, 384, 4112),
     (127, 136, 128), (128, 256, 512), (129, 264, 256), (200, 1032, 656), (256, 512, 128), (257, 256, 1024), (300, 384, 320),
     (511, 1000, 528), (513, 520, 2048), (700, 2056, 1104), (1025, 4096, 512), (2000, 2040, 784), (2049, 1024, 4096),
