@@ -69,6 +69,11 @@ def storage_bytes(rows: int, cols: int, blocksize: int = 64, dq_block: int = 256
     return a.value, b.value, c.value
 
 
+@lru_cache(maxsize=64)
+def _codebook_array(codebook: tuple):
+    return (C.c_float * 16)(*codebook)
+
+
 @dataclass
 class QuantizedNF4:
     codes: torch.Tensor      # uint8 [rows*cols/2]
@@ -84,8 +89,7 @@ class QuantizedNF4:
         s = NF4Weight()
         s.codes, s.scales, s.c2 = _ptr(self.codes), _ptr(self.scales), _ptr(self.c2)
         s.rows, s.cols, s.blocksize, s.dq_block = self.rows, self.cols, self.blocksize, self.dq_block
-        for i, v in enumerate(self.codebook):
-            s.codebook[i] = v
+        s.codebook = _codebook_array(tuple(self.codebook))
         return s
 
     @property
@@ -562,6 +566,11 @@ def linear_int8(x, w8: QuantizedInt8, out: torch.Tensor | None = None) -> torch.
     return out
 
 
+@lru_cache(maxsize=4096)
+def _bwd_bytes(T: int, N: int, K: int, r: int):
+    return saved_u_bytes(T, r), workspace_bytes(OP_BWD, T, N, K, r)
+
+
 def linear_bwd_saved_int8(dy: torch.Tensor, x8: QuantizedInt8, qw: QuantizedNF4, A: torch.Tensor, B: torch.Tensor,
                           s: float, u_saved: torch.Tensor, outs=None):
     """linear_bwd_saved with the activation kept in 8 bits (quantize_int8 of
@@ -582,10 +591,10 @@ def linear_bwd_saved_int8(dy: torch.Tensor, x8: QuantizedInt8, qw: QuantizedNF4,
             raise ValueError(f"{n} is on {t.device}, x8 on {dev}")
     _check_out("dy", dy, (T, qw.rows), dev)
     _need_cuda("u_saved", u_saved, dtype=torch.uint8)
-    if u_saved.numel() < saved_u_bytes(T, r) or u_saved.device != dev:
-        raise ValueError(f"u_saved must hold {saved_u_bytes(T, r)} bytes on {dev}")
+    u_bytes, n = _bwd_bytes(T, qw.rows, qw.cols, r)
+    if u_saved.numel() < u_bytes or u_saved.device != dev:
+        raise ValueError(f"u_saved must hold {u_bytes} bytes on {dev}")
     dx, dA, dB = _bwd_outs(outs, T, qw, r, dev)
-    n = workspace_bytes(OP_BWD, T, qw.rows, qw.cols, r)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)   # for this call only, as linear_int8's scratch
     st = qw.struct()
     _int8_call(dev, "qlora_linear_bwd_saved_int8", dy.data_ptr(), x8._ref, C.byref(st), A.data_ptr(), B.data_ptr(), r,
