@@ -125,16 +125,20 @@ def _status(device: torch.device) -> int | None:
     their scratch: made once (not while a graph is being captured) and kept."""
     st = _STATUS.get(device)
     if st is None:
-        if torch.cuda.is_current_stream_capturing():
-            return None
-        st = _STATUS[device] = torch.zeros(256, dtype=torch.uint8, device=device)
-        torch.cuda.current_stream(device).synchronize()   # other streams may be the first to use it
+        with torch.cuda.device(device):
+            if torch.cuda.is_current_stream_capturing():
+                return None
+            new = torch.zeros(256, dtype=torch.uint8, device=device)
+            torch.cuda.current_stream().synchronize()   # other streams may be the first to use it
+        st = _STATUS.setdefault(device, new)            # (two threads may come here at once)
     return st.data_ptr()
 
 
 def get_error(device=None) -> None:
     """Synchronize and raise if a kernel recorded a device-side failure."""
     dev = torch.device(device if device is not None else torch.cuda.current_device())
+    if dev.index is None:
+        dev = torch.device(dev.type, torch.cuda.current_device())
     for ws in (_WS.get(dev), _STATUS.get(dev)):
         if ws is not None:
             check("qlora_get_error", lib().qlora_get_error(C.c_void_p(ws.data_ptr()), _stream(dev)))
@@ -507,6 +511,8 @@ def quantize_int8_into(x: torch.Tensor, out: QuantizedInt8) -> QuantizedInt8:
     """Quantize x again into the buffers of an existing QuantizedInt8 of the
     same shape (no allocation)."""
     _need_cuda("x", x)
+    if not isinstance(out, QuantizedInt8):
+        raise ValueError("out must be a QuantizedInt8")
     if tuple(x.shape) != (out.rows, out.cols) or x.device != out.device:
         raise ValueError(f"x must be [{out.rows}, {out.cols}] on {out.device}")
     _int8_call(out.device, "qlora_quantize_int8", x.data_ptr(), out.rows, out.cols, out.group, out._ref)
@@ -515,6 +521,8 @@ def quantize_int8_into(x: torch.Tensor, out: QuantizedInt8) -> QuantizedInt8:
 
 def dequantize_int8(q8: QuantizedInt8, out: torch.Tensor | None = None) -> torch.Tensor:
     """BF16(code * scale) as a [rows, cols] tensor."""
+    if not isinstance(q8, QuantizedInt8):
+        raise ValueError("q8 must be a QuantizedInt8")
     dev = q8.device
     if out is None:
         out = torch.empty(q8.rows, q8.cols, dtype=torch.bfloat16, device=dev)

@@ -387,8 +387,8 @@ QLORA_API qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *o
  *   y[t, n] = BF16_RNE(RN32(RN32(float(acc) * sx[t]) * sw[n])).
  * qlora_linear_int8 quantizes x[T, K] (BF16) into `scratch` and multiplies;
  * qlora_linear_int8_q takes an already quantized x (group 0), so that several
- * products can share one.  y[T, N]: BF16, 16-byte aligned.  Results do not
- * depend on timing.  N % 8 == 0, K % 16 == 0, K <= QLORA_INT8_MAX_K (the INT32
+ * products can share one.  y[T, N]: BF16, 16-byte aligned, apart from the
+ * operands.  Results do not depend on timing.  N % 8 == 0, K % 16 == 0, K <= QLORA_INT8_MAX_K (the INT32
  * sums stay exact), T <= QLORA_INT8_MAX_T (and T * N below 2^45); T == 0 is a
  * no-op.
  * scratch: qlora_linear_int8_scratch_bytes(T, N, K) bytes, 16-byte aligned (0
@@ -411,7 +411,9 @@ QLORA_API qlora_status qlora_linear_int8_q(const qlora_int8_matrix *x, const qlo
 /*
  * qlora_linear_bwd_saved with the activation kept in 8 bits: dA = dU^T x with
  * x the values of `x` (T = x->rows rows of x->cols = K, either group), exactly
- * as coded (the scales multiply dU, nothing of x is rounded again); dX, dU and
+ * as coded (the scales multiply dU, nothing of x is rounded again; where
+ * |dU| scale leaves the FP32 range, that token's features are infinities or
+ * NaN, those whose codes are 0 among them); dX, dU and
  * dB as in qlora_linear_bwd_saved, from dy and the saved U.  The forward saves
  * U (qlora_linear_fwd_save) and the caller quantizes its x
  * (qlora_quantize_int8); x itself need not be kept, and projections that share

@@ -104,6 +104,10 @@ def test_quantize_into_and_strided_refusal():
     with pytest.raises(ValueError):
         q.quantize_int8_into(y[:39], q8)
     with pytest.raises(ValueError):
+        q.quantize_int8_into(y, q8.codes)
+    with pytest.raises(ValueError):
+        q.dequantize_int8(q8.codes)
+    with pytest.raises(ValueError):
         q.quantize_int8(x.float())
     with pytest.raises(ValueError):
         q.quantize_int8(x, group=64)
@@ -462,6 +466,10 @@ def test_status_word():
         q.get_error()
     assert e.value.status == 7
     q.get_error()
+    q._STATUS[x.device][0] = 2
+    with pytest.raises(q.QLoraError):
+        q.get_error("cuda")           # the current device
+    q.get_error()
     y = torch.empty_like(want)
     st = C.c_void_p(torch.cuda.current_stream().cuda_stream)
     assert q.lib().qlora_linear_int8_q(x8._ref, w8._ref, y.data_ptr(), None, st) == 0
@@ -485,3 +493,67 @@ def test_two_streams_at_once():
     for ys in got:
         assert all(equal_bits(a, b) for a, b in zip(ys, want))
     q.get_error()
+
+
+# --------------------------------------------------------------------------
+# matrices of more than 2^31 elements: the last rows, against calls on them alone
+# --------------------------------------------------------------------------
+def test_format_past_31_bits():
+    q = Q()
+    x = torch.empty(131200, 16400, dtype=torch.bfloat16, device="cuda").normal_()
+    for group in (0, 128):
+        q8, tail = q.quantize_int8(x, group), q.quantize_int8(x[-300:], group)
+        assert torch.equal(q8.codes[-300:], tail.codes) and torch.equal(q8.scales[:, -300:], tail.scales)
+        assert equal_bits(q.dequantize_int8(q8)[-300:], q.dequantize_int8(tail))
+        del q8
+
+
+def test_linear_int8_past_31_bits():
+    q = Q()
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def rows8(rows, cols):
+        codes = torch.empty(rows, cols, dtype=torch.int8, device="cuda").random_(-127, 128, generator=g)
+        return q.QuantizedInt8(codes, torch.rand(1, rows, device="cuda", generator=g) * 0.01)
+
+    def last(m, n):
+        return q.QuantizedInt8(m.codes[-n:], m.scales[:, -n:].clone())
+
+    w, x = rows8(40008, 65536), rows8(300, 65536)         # the weight
+    w_end = last(w, 264)
+    for T in (1, 40, 300):
+        xt = last(x, T)
+        assert equal_bits(q.linear_int8(xt, w)[:, -264:], q.linear_int8(xt, w_end))
+    w, x = rows8(16392, 64), rows8(131200, 64)            # y
+    assert equal_bits(q.linear_int8(x, w)[-300:], q.linear_int8(last(x, 300), w))
+    x, w = rows8(131200, 16400), rows8(24, 16400)         # x
+    assert equal_bits(q.linear_int8(x, w)[-300:], q.linear_int8(last(x, 300), w))
+    q.get_error()
+
+
+def test_backward_int8_past_31_bits():
+    """Only the last 200 tokens have a gradient, so dA is theirs alone: apart by
+    the BF16 rounding of both results (2^-8 each) and the order of FP32 sums of
+    200 terms and of dU's 128 (2^-24 x 328 of the terms' sizes, dU's planes 2^-16)."""
+    q = Q()
+    T, N, K, r = 131200, 128, 16384, 8
+    qw = q.quantize_nf4(inputs.normal_bf16((N, K), 0.02, 1, "cuda"))
+    A, B = inputs.normal_bf16((r, K), K ** -0.5, 2, "cuda"), inputs.normal_bf16((N, r), 0.01, 3, "cuda")
+    x = torch.empty(T, K, dtype=torch.bfloat16, device="cuda").normal_()
+    dy = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+    dy[-200:] = inputs.normal_bf16((200, N), 1.0, 4, "cuda")
+    u = torch.zeros(q.saved_u_bytes(T, r), dtype=torch.uint8, device="cuda")
+    for group in (0, 128):
+        x8 = q.quantize_int8(x, group)
+        tail = q.quantize_int8(x[-200:], group)
+        dx, dA, dB = q.linear_bwd_saved_int8(dy, x8, qw, A, B, 2.0, u)
+        tx, tA, _ = q.linear_bwd_saved_int8(dy[-200:], tail, qw, A, B, 2.0, u)
+        q.get_error()
+        du = 2.0 * dy[-200:].double() @ B.double()
+        size = du.abs().T @ q.dequantize_int8(tail).double().abs()
+        diff = (dA.double() - tA.double()).abs()
+        assert (diff <= 2 * 2.0 ** -8 * tA.double().abs() + (2.0 ** -15 + 328 * 2.0 ** -24) * size).all()
+        assert dA.abs().max() > 0 and (dx[:-200] == 0).all()
+        ddx = (dx[-200:].double() - tx.double()).abs()
+        assert (ddx <= 2 * 2.0 ** -8 * tx.double().abs() + 1e-5).all()
+        del dx, x8
