@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "quant.cu", "gemm_fwd_2sm.cu", "gemm_dx_2sm.cu", "skinny_tc.cu", "dudb.cu", "optim.cu", "decode.cu",
            "int8.cu", "int8_decode.cu", "int8_gemm.cu", "int8_gemm_2sm.cu",
            "da_int8.cu"]
-HEADERS = ["common.cuh", "gemm_common.cuh", "int8_common.cuh", "kernels.h", os.path.join("..", "..", "include", "qlora.h")]
+HEADERS = ["common.cuh", "gemm_common.cuh", "int8_common.cuh", "ring.cuh", "kernels.h", os.path.join("..", "..", "include", "qlora.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",

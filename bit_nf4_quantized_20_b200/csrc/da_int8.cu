@@ -36,6 +36,7 @@
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "ring.cuh"
 
 namespace qlora {
 
@@ -161,26 +162,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
-      int issued = 0, s = 0;
-      uint32_t ph = 1;
-      for (int st = 0; st < nst; ++st) {
-        if (s_abort || !mbar_wait_spin(rempty(s), ph, a.status)) {
-          s_abort = 1;
-          break;
-        }
-        const int32_t t = static_cast<int32_t>(tbeg + static_cast<int64_t>(st) * AT);
-        mbar_arrive_expect_tx(rfull(s), RAW);
-        tma_load_2d(raw_x(s), &tm_x, rfull(s), static_cast<int32_t>(k0), t);   // [64 t][128 k]
-        tma_load_2d(raw_q(s), &tm_hi, rfull(s), t, 0);                         // [NB j][64 t]
-        tma_load_2d(raw_q(s) + Q_BYTES, &tm_lo, rfull(s), t, 0);
-        issued = st + 1;
-        if (++s == NR) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-      if (s_abort)
-        for (int st = max(0, issued - NR); st < issued; ++st) mbar_wait(rfull(st % NR), (st / NR) & 1, a.status);
+      feed_ring(
+          0, nst, NR,
+          [&](int s, uint32_t ph) {
+            if (!s_abort && mbar_wait_spin(rempty(s), ph, a.status)) return true;
+            s_abort = 1;
+            return false;
+          },
+          [&](int s, int st) {
+            const int32_t t = static_cast<int32_t>(tbeg + static_cast<int64_t>(st) * AT);
+            mbar_arrive_expect_tx(rfull(s), RAW);
+            tma_load_2d(raw_x(s), &tm_x, rfull(s), static_cast<int32_t>(k0), t);   // [64 t][128 k]
+            tma_load_2d(raw_q(s), &tm_hi, rfull(s), t, 0);                         // [NB j][64 t]
+            tma_load_2d(raw_q(s) + Q_BYTES, &tm_lo, rfull(s), t, 0);
+          },
+          [&](int s, uint32_t ph) { return mbar_wait(rfull(s), ph, a.status); });
     }
     __syncwarp();
   } else if (warp == 1) {

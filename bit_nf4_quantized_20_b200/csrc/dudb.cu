@@ -251,13 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           issued = st + 1;
         }
       }
-      if (!ok) {
-        s_abort = 1;
-        // every copy in flight lands before the CTA can exit
-        for (int st = max(0, issued - NS); st < issued; ++st) mbar_wait(full(st % NS), (st / NS) & 1, a.status);
-        for (int c = max(0, b_issued - 2); c < b_issued; ++c) mbar_wait(b_full(c & 1), (c >> 1) & 1, a.status);
-        mbar_wait(su_full, 0, a.status);
-      }
+      if (!ok) s_abort = 1;
+      // Every copy in flight lands before the CTA leaves, whichever wait of the
+      // kernel runs out and when (see feed_ring in ring.cuh).
+      bool in = mbar_wait(su_full, 0, a.status);
+      for (int c = max(0, b_issued - 2); c < b_issued && in; ++c) in = mbar_wait(b_full(c & 1), (c >> 1) & 1, a.status);
+      for (int st = max(0, issued - NS); st < issued && in; ++st) in = mbar_wait(full(st % NS), (st / NS) & 1, a.status);
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -90,7 +90,7 @@ __device__ __forceinline__ void put_cols(uint32_t dst, int n, const uint32_t (&v
 template <int CW>
 __device__ __forceinline__ void tile_to_smem(uint32_t trow, uint32_t base, int row, int tv, bool have) {
   const uint32_t dst = base + static_cast<uint32_t>(row) * 4u;
-  if (!have) {   // a wait ran out: zeros, and the status word says so
+  if (!have) {   // a wait ran out, copies may still land here: no result, as the status word says
     for (int c = 0; c < tv; ++c)
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(c * kPitch) * 4u), "r"(0) : "memory");
     return;

@@ -27,6 +27,7 @@
 #include "gemm_common.cuh"
 #include "int8_common.cuh"
 #include "kernels.h"
+#include "ring.cuh"
 
 namespace qlora {
 
@@ -140,25 +141,18 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
-      int issued = lead, s = lead == NS ? 0 : lead;
-      uint32_t ph = lead == NS ? 0u : 1u;   // parity of the slot's last release
-      for (int st = lead; st < nst; ++st) {
-        if (s_abort || !mbar_wait_spin(empty(s), ph, a.status)) {
-          s_abort = 1;
-          break;
-        }
-        mbar_arrive_expect_tx(full(s), W_BYTES);
-        tma_load_2d(stage_w(s), &tm_w, full(s), (kb0 + st) * KB, static_cast<int32_t>(n0));
-        issued = st + 1;
-        if (++s == NS) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-      if (s_abort) {
-        // every copy in flight lands before the CTA can exit
-        for (int st = max(0, issued - NS); st < issued; ++st) mbar_wait(full(st % NS), (st / NS) & 1, a.status);
-      }
+      feed_ring(
+          lead, nst, NS,
+          [&](int s, uint32_t ph) {
+            if (!s_abort && mbar_wait_spin(empty(s), ph, a.status)) return true;
+            s_abort = 1;
+            return false;
+          },
+          [&](int s, int st) {
+            mbar_arrive_expect_tx(full(s), W_BYTES);
+            tma_load_2d(stage_w(s), &tm_w, full(s), (kb0 + st) * KB, static_cast<int32_t>(n0));
+          },
+          [&](int s, uint32_t ph) { return mbar_wait(full(s), ph, a.status); });
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -37,6 +37,7 @@
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "ring.cuh"
 
 namespace qlora {
 
@@ -183,14 +184,7 @@ __device__ __forceinline__ void skinny_tc_body(const CUtensorMap *tm_p, const CU
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
-      int issued = 0;
-      for (int st = 0; st < nst; ++st) {
-        const int s = st % NS;
-        const uint32_t ph = (st / NS) & 1;
-        if (s_abort || !mbar_wait(empty(s), ph ^ 1, a.status)) {
-          s_abort = 1;
-          break;
-        }
+      auto issue = [&](int s, int st) {
         const int32_t c0 = static_cast<int32_t>(cbeg + static_cast<int64_t>(st) * TBK);
         mbar_arrive_expect_tx(full(s), stage_bytes);
         if (!a.p_col) {
@@ -208,12 +202,15 @@ __device__ __forceinline__ void skinny_tc_body(const CUtensorMap *tm_p, const CU
               tma_load_2d(stage_q(s, qi) + h * (TBK * 128), tq, full(s), h * 64, c0);                 // [64 c][64 j]
           }
         }
-        issued = st + 1;
-      }
-      if (s_abort) {
-        for (int st = max(0, issued - NS); st < issued; ++st)
-          mbar_wait(full(st % NS), (st / NS) & 1, a.status);
-      }
+      };
+      feed_ring(
+          0, nst, NS,
+          [&](int s, uint32_t ph) {
+            if (!s_abort && mbar_wait(empty(s), ph, a.status)) return true;
+            s_abort = 1;
+            return false;
+          },
+          issue, [&](int s, uint32_t ph) { return mbar_wait(full(s), ph, a.status); });
     }
     __syncwarp();
   } else if (warp == 1) {
