@@ -38,6 +38,22 @@ __device__ __forceinline__ bool named_bar_any(int id, int count, bool pred) {
   return r != 0;
 }
 
+// At the end of a pair kernel, after the CTA's last __syncthreads: if one of its
+// waits ran out, TMA loads may still be on their way into its shared memory.
+// Their completion is counted in the even CTA's barriers, on which the other
+// CTA cannot wait, so the CTA stays for 2 ms, a thousand times what a load
+// takes.  `aborted` covers every such case: a CTA whose epilogue saw all its
+// accumulators complete has had every load consumed, and one whose epilogue did
+// not has set it, whichever warp's wait ran out first.
+__device__ __forceinline__ void settle_loads(bool aborted) {
+  if (aborted) {
+    const uint64_t t_end = globaltimer() + 2000000ull;
+    while (globaltimer() < t_end) {
+    }
+  }
+  __syncwarp();
+}
+
 // A work unit of a CTA pair: weight-side tile m_pair (256 rows of the MMA's
 // M side) against tokens tok0 .. tok0 + ntok - 1 (ntok = 256, or 128 for a
 // half tile).

@@ -243,15 +243,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         grid_dep_wait();
         grid_dep_launch();
       }
-      if (!ok) {
-        s_abort = 1;
-        // loads still in flight land in this CTA's shared memory; give them time to
-        // finish (their completion is counted in the leader's barrier, which this
-        // CTA cannot wait on)
-        const uint64_t t_end = globaltimer() + 2000000ull;
-        while (globaltimer() < t_end) {
-        }
-      }
+      if (!ok) s_abort = 1;
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -365,6 +357,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  settle_loads(s_abort != 0);
   cluster_arrive_wait();   // both CTAs are done with the pair's tensor memory
   if (warp == 17) {
     tc_fence_after();

@@ -121,3 +121,19 @@ def test_no_copy_is_in_flight_when_the_producer_returns(tmp_path):
 def test_the_one_cta_kernels_use_it(name):
     with open(os.path.join(CSRC, name)) as f:
         assert f.read().count("feed_ring(") == 1
+
+
+@pytest.mark.parametrize("name", ["int8_gemm_2sm.cu", "gemm_fwd_2sm.cu", "gemm_dx_2sm.cu"])
+def test_the_pair_kernels_settle_after_their_last_barrier(name):
+    """A pair kernel's loads are counted in the other CTA's barriers too, so it
+    gives them time instead -- where any warp's wait ran out, not the
+    producer's alone: after the barrier that brings all warps' findings
+    together, and before the CTA may leave."""
+    with open(os.path.join(CSRC, name)) as f:
+        code = [line.split("//")[0].strip() for line in f]
+    code = [line for line in code if line]
+    at = [i for i, line in enumerate(code) if line.startswith("settle_loads(")]
+    assert [code[i] for i in at] == ["settle_loads(s_abort != 0);"]
+    assert code[at[0] - 1] == "__syncthreads();" and code[at[0] + 1] == "cluster_arrive_wait();"
+    # every role that stops early has said so before that barrier
+    assert sum(line == "if (!ok) s_abort = 1;" for line in code[:at[0]]) >= 3
