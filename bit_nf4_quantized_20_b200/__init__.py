@@ -107,9 +107,15 @@ def workspace_bytes(op: int, T: int, N: int, K: int, r: int) -> int:
 _WS: dict = {}
 
 
+def _indexed(device) -> torch.device:
+    """`device` with its index: "cuda" is the current device."""
+    dev = torch.device(device)
+    return torch.device("cuda", torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev
+
+
 def workspace(device: torch.device, nbytes: int) -> torch.Tensor:
     """A zeroed, 256-byte aligned workspace of at least nbytes on `device` (cached, grows)."""
-    key = torch.device(device)
+    key = _indexed(device)
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 4096), dtype=torch.uint8, device=key)
@@ -136,9 +142,7 @@ def _status(device: torch.device) -> int | None:
 
 def get_error(device=None) -> None:
     """Synchronize and raise if a kernel recorded a device-side failure."""
-    dev = torch.device(device if device is not None else torch.cuda.current_device())
-    if dev.index is None:
-        dev = torch.device(dev.type, torch.cuda.current_device())
+    dev = _indexed(device if device is not None else torch.cuda.current_device())
     for ws in (_WS.get(dev), _STATUS.get(dev)):
         if ws is not None:
             check("qlora_get_error", lib().qlora_get_error(C.c_void_p(ws.data_ptr()), _stream(dev)))
