@@ -120,15 +120,19 @@ def workspace(device: torch.device, nbytes: int) -> torch.Tensor:
 
 
 _STATUS: dict = {}
+_FIXED: set = set()   # devices of which a call was given no word: the library's fixed array holds it
 
 
 def _status(device: torch.device) -> int | None:
     """Address of `device`'s status word for the calls that take it apart from
-    their scratch: made once (not while a graph is being captured) and kept."""
+    their scratch: made once and kept.  None while a graph is being captured
+    (memory from its pool would be zeroed by every replay): the call then
+    records in the library's fixed array, and get_error looks there too."""
     st = _STATUS.get(device)
     if st is None:
         with torch.cuda.device(device):
             if torch.cuda.is_current_stream_capturing():
+                _FIXED.add(device)
                 return None
             new = torch.zeros(256, dtype=torch.uint8, device=device)
             torch.cuda.current_stream().synchronize()   # other streams may be the first to use it
@@ -142,6 +146,8 @@ def get_error(device=None) -> None:
     for ws in (_WS.get(dev), _STATUS.get(dev)):
         if ws is not None:
             check("qlora_get_error", lib().qlora_get_error(C.c_void_p(ws.data_ptr()), _stream(dev)))
+    if dev in _FIXED:
+        noalloc_get_error(dev)
 
 
 def quantize_nf4(w: torch.Tensor, codebook=None, blocksize: int = 64, dq_block: int = 256,

@@ -1348,6 +1348,12 @@ qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *out_bf16, v
              : QLORA_ERR_CUDA;
 }
 
+// The word that a call records its timeouts in: the caller's, or that of the
+// allocation-free forward's fixed array.
+static uint32_t *status_word(void *status) {
+  return static_cast<uint32_t *>(status ? status : noalloc_scratch_ptr());
+}
+
 // Checks of both int8 products: the weight, the token count and the output.
 static qlora_status check_linear_int8(int64_t T, int64_t K, const qlora_int8_matrix *w, const void *y,
                                       const void *status) {
@@ -1372,7 +1378,7 @@ struct Int8Launch {
 };
 
 static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, const qlora_int8_matrix *w, void *y,
-                                 void *status, bool early, Int8Launch &l) {
+                                 uint32_t *status, bool early, Int8Launch &l) {
   const int64_t N = w->rows, K = w->cols;
   l.g = int8_gemm_geom(T, N, K, kSplitSms);
   memset(&l.a, 0, sizeof(l.a));
@@ -1386,7 +1392,7 @@ static qlora_status prepare_int8(const int8_t *xq, const float *sx, int64_t T, c
   l.a.stages = l.g.stages;
   l.a.kb_per_split = l.g.kb_per_split;
   l.a.early = early && g_trace.recs == nullptr ? 1 : 0;
-  l.a.status = static_cast<uint32_t *>(status);
+  l.a.status = status;
   l.p.T = T;
   l.p.N = N;
   l.p.K = K;
@@ -1427,6 +1433,8 @@ qlora_status qlora_linear_int8(const void *x_bf16, int64_t T, const qlora_int8_m
   if (!aligned16(x_bf16)) return QLORA_ERR_MISALIGNED;
   const int64_t N = w->rows, K = w->cols;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint32_t *word = status_word(status);
+  if (!word) return QLORA_ERR_CUDA;
   Int8DecodeGeom g;
   if (int8_decode_geom(T, N, K, kSplitSms, g)) {
     Int8DecodeArgs a;
@@ -1439,7 +1447,7 @@ qlora_status qlora_linear_int8(const void *x_bf16, int64_t T, const qlora_int8_m
     a.y = static_cast<uint16_t *>(y);
     a.stages = g.stages;
     a.kb_per_split = g.kb_per_split;
-    a.status = static_cast<uint32_t *>(status);
+    a.status = word;
     CUtensorMap m_w;
     if (!make_map_u8(&m_w, w->codes, N, K, K, 128, 128)) return QLORA_ERR_CUDA;
     const double n = static_cast<double>(N), k = static_cast<double>(K);
@@ -1451,7 +1459,7 @@ qlora_status qlora_linear_int8(const void *x_bf16, int64_t T, const qlora_int8_m
   int8_t *xq = static_cast<int8_t *>(scratch);
   float *sx = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + round_up(T * K, 256));
   Int8Launch l;
-  cs = prepare_int8(xq, sx, T, w, y, status, true, l);
+  cs = prepare_int8(xq, sx, T, w, y, word, true, l);
   if (cs != QLORA_OK) return cs;
   cs = run_quantize_int8(x_bf16, T, K, 0, xq, sx, st);
   if (cs != QLORA_OK) return cs;
@@ -1466,8 +1474,10 @@ qlora_status qlora_linear_int8_q(const qlora_int8_matrix *x, const qlora_int8_ma
   if (cs != QLORA_OK) return cs;
   if (x->group != 0) return QLORA_ERR_UNSUPPORTED;   // the product takes one scale a token
   if (x->rows == 0) return QLORA_OK;
+  uint32_t *word = status_word(status);
+  if (!word) return QLORA_ERR_CUDA;
   Int8Launch l;
-  cs = prepare_int8(x->codes, x->scales, x->rows, w, y, status, false, l);
+  cs = prepare_int8(x->codes, x->scales, x->rows, w, y, word, false, l);
   if (cs != QLORA_OK) return cs;
   return launch_int8(l, static_cast<cudaStream_t>(stream));
 }
@@ -1493,8 +1503,9 @@ qlora_status qlora_linear_bwd_saved_int8(const void *dy, const qlora_int8_matrix
     if (cudaMemsetAsync(dB, 0, static_cast<size_t>(N) * r * 2, st) != cudaSuccess) return QLORA_ERR_CUDA;
     return QLORA_OK;
   }
-  return linear_bwd_impl(dy, nullptr, x, T, qw, A, B, r, s, u_saved, dx, dA, dB, ws, static_cast<uint32_t *>(status),
-                         st);
+  uint32_t *word = status_word(status);
+  if (!word) return QLORA_ERR_CUDA;
+  return linear_bwd_impl(dy, nullptr, x, T, qw, A, B, r, s, u_saved, dx, dA, dB, ws, word, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -396,8 +396,9 @@ QLORA_API qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *o
  * them itself: then scratch may be NULL); it need not be initialised and holds
  * nothing between calls, but calls that may overlap must not share it.
  * status: a status word as at the start of a workspace (zeroed once, read by
- * qlora_get_error(status, stream)); any number of calls may share it; NULL: a
- * bounded wait that runs out is not reported.
+ * qlora_get_error(status, stream)); any number of calls may share it; NULL:
+ * the word of qlora_linear_fwd_noalloc's fixed array on the current device
+ * (read by qlora_noalloc_get_error), which needs no memory of the caller's.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
  */
 #define QLORA_INT8_MAX_K 131072

@@ -17,6 +17,13 @@ class FakeLib:
             return 7
         return 0
 
+    def qlora_noalloc_get_error(self, stream):
+        self.polled.append("fixed")
+        if "fixed" in self.set:
+            self.set.discard("fixed")
+            return 7
+        return 0
+
     def qlora_status_string(self, code):
         return b"timeout"
 
@@ -29,6 +36,7 @@ def q(monkeypatch):
     monkeypatch.setattr(q._lib, "lib", lambda: fake)
     monkeypatch.setattr(q, "_WS", {})
     monkeypatch.setattr(q, "_STATUS", {})
+    monkeypatch.setattr(q, "_FIXED", set(), raising=False)
     monkeypatch.setattr(q, "_stream", lambda dev: None)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k))
@@ -58,3 +66,27 @@ def test_another_device_has_a_word_of_its_own(q):
     q.get_error("cuda")            # device 1: nothing recorded there
     with pytest.raises(q.QLoraError):
         q.get_error("cuda:0")
+
+
+def test_a_first_use_inside_a_capture_is_reported(q, monkeypatch):
+    """No word can be made while a graph is captured.  The call then records in
+    the library's fixed array (a null word), and get_error reads that as well."""
+    from contextlib import nullcontext
+    dev = torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    assert q._status(dev) is None
+    q.fake.set.add("fixed")
+    q.get_error("cuda:0")                  # another device: not its array
+    assert q.fake.polled == []
+    with pytest.raises(q.QLoraError) as e:
+        q.get_error()
+    assert e.value.status == 7
+    q.get_error()
+    # a word made later does not hide what the graph's replays record
+    word = torch.zeros(256, dtype=torch.uint8)
+    q._STATUS[dev] = word
+    assert q._status(dev) == word.data_ptr()
+    q.fake.set.add("fixed")
+    with pytest.raises(q.QLoraError):
+        q.get_error()
