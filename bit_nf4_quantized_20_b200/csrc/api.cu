@@ -1258,19 +1258,26 @@ qlora_status qlora_noalloc_get_error(void *stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Failure-detection self-test: one thread waits, with the same bounded wait
-// every pipeline of the library uses, on an mbarrier that no thread arrives on.
-// The wait gives up after limit_ns and records DEV_TIMEOUT in the status word.
+// Failure-detection self-test: one thread waits, with each of the two bounded
+// waits that the library's pipelines use, on an mbarrier that no thread arrives
+// on.  Each gives up after limit_ns; DEV_TIMEOUT is recorded in the status word
+// if both say so and both recorded it.
 // ---------------------------------------------------------------------------
 static __global__ void wait_selftest_kernel(uint32_t *status, uint64_t limit_ns) {
   __shared__ __align__(8) uint64_t bar;
+  __shared__ uint32_t word[2];
   if (threadIdx.x == 0) {
+    word[0] = word[1] = 0;
     mbar_init(smem_u32(&bar), 1);
     fence_mbar_init();
   }
   __syncthreads();
   // parity 0 of a fresh barrier completes only after one arrival, which never comes
-  if (threadIdx.x == 0) mbar_wait(smem_u32(&bar), 0, status, limit_ns);
+  if (threadIdx.x == 0) {
+    const bool a = mbar_wait(smem_u32(&bar), 0, &word[0], limit_ns);
+    const bool b = mbar_wait_spin(smem_u32(&bar), 0, &word[1], limit_ns);
+    if (!a && !b && word[0] == DEV_TIMEOUT && word[1] == DEV_TIMEOUT) set_status(status, DEV_TIMEOUT);
+  }
   __syncthreads();
 }
 

@@ -431,10 +431,11 @@ QLORA_API qlora_status qlora_linear_bwd_saved_int8(const void *dy, const qlora_i
 
 /*
  * Failure-detection self-test (a diagnostic; the pages have no counterpart).
- * Launches one kernel whose thread waits, with the bounded mbarrier wait that
- * every pipeline of the library uses, on a barrier that nothing arrives on;
- * after limit_us microseconds the wait gives up, records the timeout in the
- * workspace's status word and the kernel returns.  qlora_get_error(ws, stream)
+ * Launches one kernel whose thread waits, with each of the two bounded mbarrier
+ * waits that the library's pipelines use (one suspends the thread between its
+ * probes, one does not), on a barrier that nothing arrives on; each gives up
+ * after limit_us microseconds, the timeout is recorded in the workspace's
+ * status word if both did, and the kernel returns.  qlora_get_error(ws, stream)
  * then returns QLORA_ERR_TIMEOUT.  The kernels' own waits keep their 2 s
  * limit.  limit_us in [1, 2000000]; ws: at least 256 bytes, 256-byte aligned,
  * or NULL for the fixed array of qlora_linear_fwd_noalloc on the current device

@@ -3,6 +3,7 @@ import os
 import subprocess
 import sys
 import threading
+import time
 
 import pytest
 import torch
@@ -101,3 +102,24 @@ def test_a_null_word_is_the_fixed_arrays():
     q._int8_call(x8.device, "qlora_linear_int8_q", x8._ref, w8._ref, y.data_ptr(), None)
     q.noalloc_get_error()
     assert torch.equal(y.view(torch.int16), q.linear_int8(x8, w8).view(torch.int16))
+
+
+def test_both_bounded_waits_run_out():
+    """The two waits of the pipelines (the 8-bit kernels' producers and issuers
+    use the one that does not suspend) give up one after the other, each after
+    its limit, and the 8-bit calls' status word says so once."""
+    q = Q()
+    dev = torch.device("cuda", torch.cuda.current_device())
+    w8 = q.quantize_int8(inputs.normal_bf16((64, 256), 0.02, 2, "cuda"))
+    x = inputs.normal_bf16((40, 256), 1.0, 1, "cuda")
+    want = q.linear_int8(x, w8)
+    q.get_error()
+    limit_us = 20000
+    t0 = time.perf_counter()
+    assert q.lib().qlora_wait_selftest(q._status(dev), 256, limit_us, q._raw_stream(dev.index)) == 0
+    with pytest.raises(q.QLoraError) as e:
+        q.get_error()
+    assert e.value.status == 7
+    assert 2e-6 * limit_us <= time.perf_counter() - t0 < 5.0
+    q.get_error()
+    assert torch.equal(q.linear_int8(x, w8).view(torch.int16), want.view(torch.int16))
