@@ -428,7 +428,9 @@ class QuantizedInt8:
     """A matrix in signed 8-bit codes (qlora_int8_matrix): value = code * scale,
     one FP32 scale per row (group 0) or per 128 consecutive columns of a row
     (group 128).  codes: int8 [rows, cols]; scales: float32 [groups, rows]; the
-    attributes are read-only (the buffers' contents are not)."""
+    attributes are read-only (the buffers' contents are not).  quantize_int8
+    writes codes from -127 to 127; -128 in given codes is taken as well, but a
+    product over 131072 columns that are -128 on both sides leaves INT32."""
 
     __slots__ = ("_codes", "_scales", "_rows", "_cols", "_group", "_device", "_struct", "_ref")
 

@@ -383,7 +383,9 @@ QLORA_API qlora_status qlora_dequantize_int8(const qlora_int8_matrix *m, void *o
  * The int8 product of a merged weight (qlora_merge_adapter, then
  * qlora_quantize_int8 with group 0: one scale per output channel) with
  * activations quantized per token:
- *   acc[t, n] = sum_k xq[t, k] wq[n, k] in INT32, exact;
+ *   acc[t, n] = sum_k xq[t, k] wq[n, k] in INT32, exact (codes written by the
+ *   caller may hold -128 too, which the quantizer never writes: of all sums only
+ *   131072 products of -128 by -128, 2^31, do not fit and come out negative);
  *   y[t, n] = BF16_RNE(RN32(RN32(float(acc) * sx[t]) * sw[n])).
  * qlora_linear_int8 quantizes x[T, K] (BF16) into `scratch` and multiplies;
  * qlora_linear_int8_q takes an already quantized x (group 0), so that several

@@ -1,5 +1,5 @@
 """Cases of the 8-bit operators whose results are exact, so that nothing can
-hide in a tolerance: the second planes of dU."""
+hide in a tolerance: the second planes of dU, and codes of -128."""
 import numpy as np
 import pytest
 import torch
@@ -112,3 +112,71 @@ def test_dA_from_the_low_planes_alone(T, N, K, r, group):
     _, dA, _ = q.linear_bwd_saved_int8(tY, x8, qw, tA, tB, 1.0, u)
     q.get_error()
     assert np.array_equal(bits(dA), bf16_of(want)), f"{(bits(dA) != bf16_of(want)).sum()} of {dA.numel()} differ"
+
+
+# --------------------------------------------------------------------------
+# the whole range of a signed byte
+# --------------------------------------------------------------------------
+def low_codes(rows, cols, seed, everywhere):
+    """Given codes with -128, which quantize_int8 never writes."""
+    rng = np.random.default_rng(seed)
+    c = np.full((rows, cols), -128) if everywhere else rng.integers(-128, 128, (rows, cols))
+    c[:, :3] = -128
+    s = (2.0 ** rng.integers(-12, -2, (1, rows))).astype(np.float32)
+    return c.astype(np.int8), s
+
+
+def given(c, s, group=0):
+    return Q().QuantizedInt8(torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda(), group)
+
+
+@pytest.mark.parametrize("everywhere", [False, True])
+@pytest.mark.parametrize("T,N,K", [(3, 16, 131056), (40, 16, 131056), (100, 264, 1040), (600, 520, 2064)])
+def test_product_of_given_codes(T, N, K, everywhere):
+    """Sums up to 16384 K: inside INT32 for every K but the largest."""
+    q = Q()
+    (xc, xs), (wc, ws) = low_codes(T, K, 1, everywhere), low_codes(N, K, 2, everywhere)
+    y = q.linear_int8(given(xc, xs), given(wc, ws))
+    q.get_error()
+    assert np.array_equal(bits(y), O.linear_int8(xc, xs[0], wc, ws[0]))
+    if everywhere and K == 131056:
+        assert (np.abs(f64(y)) > 0).all() and (y > 0).all()
+
+
+def test_largest_length_of_codes_that_quantize_writes():
+    """K = 131072 with -128 on one side alone: 128 x 127 x K is inside INT32."""
+    q = Q()
+    T, N, K = 33, 8, 131072
+    xc, xs = low_codes(T, K, 1, True)
+    wc, ws = np.full((N, K), 127, np.int8), np.full((1, N), 2.0 ** -6, np.float32)
+    wc[1::2] = -127
+    y = q.linear_int8(given(xc, xs), given(wc, ws))
+    assert np.array_equal(bits(y), O.linear_int8(xc, xs[0], wc, ws[0]))
+    # tokens quantized in the call against -128 in the weight
+    x = torch.ones(2, K, dtype=torch.bfloat16, device="cuda")
+    wl = given(np.full((N, K), -128, np.int8), ws)
+    want = O.linear_int8(np.full((2, K), 127, np.int8), np.full(2, np.float32(1) / np.float32(127), np.float32),
+                         np.full((N, K), -128, np.int8), ws[0])
+    assert np.array_equal(bits(q.linear_int8(x, wl)), want)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_restored_and_backward_of_given_codes(group):
+    """-128 in a checkpoint: restored, and in dA, as what it stands for.  dU is
+    1 or -1 and the scales are powers of two, so the sums are exact."""
+    q = Q()
+    T, N, K, r = 70, 64, 192, 9
+    rng = np.random.default_rng(5)
+    c, _ = low_codes(T, K, 3, False)
+    groups = -(-K // 128) if group else 1
+    s = (2.0 ** rng.integers(-3, 3, (groups, T))).astype(np.float32)
+    x8 = given(c, s, group)
+    x = c * np.repeat(s.T.astype(np.float64), group or K, axis=1)[:, :K]
+    assert np.array_equal(f64(q.dequantize_int8(x8)), x)
+    dY, B, A = np.zeros((T, N)), np.zeros((N, r)), np.zeros((r, K))
+    dY[:, 5], B[5] = rng.choice([-1.0, 1.0], T), rng.choice([-1.0, 1.0], r)
+    qw = q.quantize_nf4(inputs.normal_bf16((N, K), 0.02, 3, "cuda"))
+    u = torch.zeros(q.saved_u_bytes(T, r), dtype=torch.uint8, device="cuda")
+    _, dA, dB = q.linear_bwd_saved_int8(dev_bf16(dY), x8, qw, dev_bf16(A), dev_bf16(B), 1.0, u)
+    q.get_error()
+    assert np.array_equal(bits(dA), bf16_of((dY @ B).T @ x)) and not dB.any()
