@@ -69,7 +69,7 @@ enum KernelId : int32_t {
   K_LORA_DU_DB = 12,    // dU and dB from one read of dY (block partial sums)
   K_ADAM = 13,          // the adapters' optimizer step
   K_LORA_DU_DB_SUM = 14,  // the sums of those partials: dU planes and dB
-  K_UNUSED = 15,        // callers tell an id past the NF4 layer's kernels by this number
+  K_UNUSED = 15,        // no kernel: qlora_kernel_name(15) has always been "unknown", and stays so
   K_QUANTIZE_INT8 = 16,
   K_DEQUANTIZE_INT8 = 17,
   K_INT8_GEMM = 18,
