@@ -14,10 +14,14 @@
 //
 // With a few tokens the weights' bytes are the cost, so they load before the
 // dependency wait when only the activations come from the kernel before.
-// Bound by that stream for a few tokens, by the tokens that every row tile reads
-// again from L2 for 64 to 512.  With the quantizing launch: 16 tokens on
-// 14336 x 4096 14.6 us (4.0 TB/s; 9.1 of it the stream at the copy rate), 101 on
-// 4096 x 14336 19.0 us.
+// For a few tokens the weights' stream bounds it, between a start and a sum that
+// are fixed, over SMs that hold two or three CTAs each.  From 64 to 512 no rate
+// does: 101 tokens on 4096 x 14336 use 38 % of DRAM, 27 % of L2, 22 % of the
+// tensor pipe; about half the time is the start of two CTAs an SM and the
+// cluster's sum (7.0 us in int8_gemm_geom's estimate of 14.6).  With the
+// quantizing launch and without: 16 tokens on 14336 x 4096 14.6 and 13.5 us
+// (4.0 TB/s; 9.1 of it the stream at the copy rate), 101 on 4096 x 14336 18.8
+// and 17.4 us.
 //
 // Warps: 0 TMA producer, 1 tensor-memory allocation + MMA issue, 2-5 epilogue.
 

@@ -14,9 +14,9 @@
 //
 // Bound by the tensor cores; the tiles run in blocks of eight weight tiles by
 // all token tiles, so that the pairs running at one time share operands in L2.
-// 4096 tokens on 14336 x 4096: 145.8 us, 3.30 Pop/s, twice the measured BF16
-// rate, tensor pipe active 93 % of the cycles; in a long run the power cap
-// lowers the clock and it takes 180.
+// 4096 tokens on 14336 x 4096: 145.8 us, 3.30 Pop/s, tensor pipe active 92 to
+// 93 % of the cycles in which an SM is (86 % of all) at 1.62 GHz; in a long run
+// the power cap lowers the clock further and it takes 180.
 //
 // Warps: 0-7 epilogue, 8 TMA, 9 paired tensor-memory allocation and, on the
 // even CTA, the MMA issue.
